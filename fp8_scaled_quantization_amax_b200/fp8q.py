@@ -52,6 +52,13 @@ SIGNATURES = {
     "fp8_gemm_block_e8m0_requant": (_S, [_P, _I, _P, _I, _I64, _I64, _I64, _P, _P, _P, _I64, _I, _P, _P, _P, _P]),
     "fp8_paged_kv_write": (_S, [_P, _P, _I64, _I64, _I64, _I64, _I, _P, _P, _P]),
     "fp8_paged_kv_gather": (_S, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I, _P, _P]),
+    "fp8_paged_attention_decode": (_S, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _P, _P, _I64,
+                                        _I64, _I64, _F, _P, _P, _P, _I64, _F, _P, ctypes.c_size_t, _P]),
+    "fp8_paged_attention_prefill": (_S, [_P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I,
+                                         _P, _P, _I64, _I64, _I64, _F, _P, _P, _P, ctypes.c_size_t, _P]),
+    "fp8_paged_attention_workspace_size": (_S, [_I64, _I64, _I64, _I64, _I64, _I, _I64, _P]),
+    "fp8_paged_kv_evict": (_S, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _I64,
+                                _I64, _I64, _P, _P, _I64, _P, _P]),
     "fp8_scale_stats": (_S, [_P, _P, _I64, _P, _I64, _F, _P, _P, _P]),
     "fp8_device_error": (_S, [_P, _I]),
 }
@@ -117,6 +124,29 @@ def _dev(t, dtype, what):
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
+
+
+def _same_device(first, **others):
+    """Every tensor on the device of `first`: the library runs on that device."""
+    for what, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{what}: on {t.device}, expected {first.device}")
+
+
+def _token_rows(t, what):
+    """bf16 [T, heads, Dh] whose tokens may lie apart (a slice of a fused projection); its token stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{what}: expected [tokens, heads, Dh]")
+    T, Hq, Dh = t.shape
+    if t.numel() and ((Dh > 1 and t.stride(2) != 1) or (Hq > 1 and t.stride(1) != Dh)):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    return t.stride(0) if T > 1 else Hq * Dh
 
 
 # ------------------------------------------------------- raw entry points --
@@ -350,6 +380,66 @@ def fp8_paged_kv_gather(cache, scale_cache, block_table, seq_lens, B, max_blocks
         num_blocks, S_out, fmt, _ptr(out), _stream(stream)))
 
 
+def fp8_paged_attention_decode(q, ld_q, B, Hq, k_cache, k_scale, v_cache, v_scale, H, Dh, block_size, num_blocks, fmt,
+                               block_table, seq_lens, max_blocks, window, sinks, softmax_scale, out, lse=None,
+                               mass=None, ld_mass=0, mass_decay=1.0, workspace=None, stream=None):
+    _token_rows(q, "q"); _dev(k_cache, torch.uint8, "k_cache"); _dev(v_cache, torch.uint8, "v_cache")
+    _dev(k_scale, torch.float32, "k_scale"); _dev(v_scale, torch.float32, "v_scale")
+    _dev(block_table, torch.int32, "block_table"); _dev(seq_lens, torch.int32, "seq_lens")
+    _dev(out, torch.bfloat16, "out"); _dev(lse, torch.float32, "lse"); _dev(mass, torch.float32, "mass")
+    _dev(workspace, torch.uint8, "workspace")
+    _same_device(q, k_cache=k_cache, k_scale=k_scale, v_cache=v_cache, v_scale=v_scale, block_table=block_table,
+                 seq_lens=seq_lens, out=out, lse=lse, mass=mass, workspace=workspace)
+    with torch.cuda.device(q.device):
+        _check("fp8_paged_attention_decode", lib().fp8_paged_attention_decode(
+            _ptr(q), ld_q, B, Hq, _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), H, Dh, block_size,
+            num_blocks, fmt, _ptr(block_table), _ptr(seq_lens), max_blocks, window, sinks, softmax_scale, _ptr(out),
+            _ptr(lse), _ptr(mass), ld_mass, mass_decay, _ptr(workspace), 0 if workspace is None else workspace.numel(),
+            _stream(stream)))
+
+
+def fp8_paged_attention_prefill(q, ld_q, T, q_offsets, B, Hq, k_cache, k_scale, v_cache, v_scale, H, Dh, block_size,
+                                num_blocks, fmt, block_table, seq_lens, max_blocks, window, sinks, softmax_scale, out,
+                                lse=None, workspace=None, stream=None):
+    _token_rows(q, "q"); _dev(k_cache, torch.uint8, "k_cache"); _dev(v_cache, torch.uint8, "v_cache")
+    _dev(k_scale, torch.float32, "k_scale"); _dev(v_scale, torch.float32, "v_scale")
+    _dev(q_offsets, torch.int64, "q_offsets"); _dev(block_table, torch.int32, "block_table")
+    _dev(seq_lens, torch.int32, "seq_lens"); _dev(out, torch.bfloat16, "out"); _dev(lse, torch.float32, "lse")
+    _dev(workspace, torch.uint8, "workspace")
+    _same_device(q, q_offsets=q_offsets, k_cache=k_cache, k_scale=k_scale, v_cache=v_cache, v_scale=v_scale,
+                 block_table=block_table, seq_lens=seq_lens, out=out, lse=lse, workspace=workspace)
+    with torch.cuda.device(q.device):
+        _check("fp8_paged_attention_prefill", lib().fp8_paged_attention_prefill(
+            _ptr(q), ld_q, T, _ptr(q_offsets), B, Hq, _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), H,
+            Dh, block_size, num_blocks, fmt, _ptr(block_table), _ptr(seq_lens), max_blocks, window, sinks,
+            softmax_scale, _ptr(out), _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+            _stream(stream)))
+
+
+def fp8_paged_attention_workspace_size(B, Hq, H, Dh, max_context, weights, tokens) -> int:
+    b = ctypes.c_size_t(0)
+    _check("fp8_paged_attention_workspace_size", lib().fp8_paged_attention_workspace_size(
+        B, Hq, H, Dh, max_context, int(weights), tokens, ctypes.byref(b)))
+    return int(b.value)
+
+
+def fp8_paged_kv_evict(k_cache, k_scale, v_cache, v_scale, H, Dh, block_size, num_blocks, block_table, seq_lens, B,
+                       max_blocks, mass, ld_mass, dst_table, dst_max_blocks, budget, sinks, recent, kept, mass_out,
+                       ld_out, lens_out, stream=None):
+    _dev(k_cache, torch.uint8, "k_cache"); _dev(v_cache, torch.uint8, "v_cache")
+    _dev(k_scale, torch.float32, "k_scale"); _dev(v_scale, torch.float32, "v_scale")
+    _dev(block_table, torch.int32, "block_table"); _dev(seq_lens, torch.int32, "seq_lens")
+    _dev(mass, torch.float32, "mass"); _dev(dst_table, torch.int32, "dst_table"); _dev(kept, torch.int32, "kept")
+    _dev(mass_out, torch.float32, "mass_out"); _dev(lens_out, torch.int32, "lens_out")
+    _same_device(k_cache, k_scale=k_scale, v_cache=v_cache, v_scale=v_scale, block_table=block_table,
+                 seq_lens=seq_lens, mass=mass, dst_table=dst_table, kept=kept, mass_out=mass_out, lens_out=lens_out)
+    with torch.cuda.device(k_cache.device):
+        _check("fp8_paged_kv_evict", lib().fp8_paged_kv_evict(
+            _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), H, Dh, block_size, num_blocks,
+            _ptr(block_table), _ptr(seq_lens), B, max_blocks, _ptr(mass), ld_mass, _ptr(dst_table), dst_max_blocks,
+            budget, sinks, recent, _ptr(kept), _ptr(mass_out), ld_out, _ptr(lens_out), _stream(stream)))
+
+
 def fp8_scale_stats(scales, prev, n, seg_offsets, num_segments, jump_ratio, stats, counts, stream=None):
     _dev(scales, torch.float32, "scales"); _dev(prev, torch.float32, "prev")
     _dev(seg_offsets, torch.int64, "seg_offsets")
@@ -468,6 +558,18 @@ class PagedKVCache:
         self.cache = torch.zeros((num_blocks, block_size, H, Dh), dtype=torch.uint8, device=device)
         self.scale_inv = torch.zeros((num_blocks, block_size, H), dtype=torch.float32, device=device)
 
+    @classmethod
+    def from_tensors(cls, cache, scale_inv, fmt: int = E4M3):
+        """The cache over buffers the caller holds: codes [num_blocks, block_size, H, Dh] uint8 and 1/s
+        [num_blocks, block_size, H] fp32."""
+        _dev(cache, torch.uint8, "cache"); _dev(scale_inv, torch.float32, "scale_inv")
+        if cache.dim() != 4 or scale_inv.shape != cache.shape[:3]:
+            raise ValueError("expected cache [num_blocks, block_size, H, Dh] and scale_inv [num_blocks, block_size, H]")
+        self = cls.__new__(cls)
+        self.fmt, self.cache, self.scale_inv = fmt, cache, scale_inv
+        self.num_blocks, self.block_size, self.H, self.Dh = cache.shape
+        return self
+
     def write(self, kv, slot_mapping):
         """kv [T, H, Dh] bf16 into the slots slot_mapping [T] (int64; < 0 = padding)."""
         T = kv.shape[0]
@@ -481,6 +583,100 @@ class PagedKVCache:
         fp8_paged_kv_gather(self.cache, self.scale_inv, block_table, seq_lens, B, mb, self.H, self.Dh,
                             self.block_size, self.num_blocks, S_out, self.fmt, out)
         return out
+
+
+def _kv_pair(k_cache, v_cache):
+    same = ("fmt", "block_size", "H", "Dh", "num_blocks")
+    if any(getattr(k_cache, a) != getattr(v_cache, a) for a in same):
+        raise ValueError("the K and V caches must have the same format and shape")
+    return (k_cache.cache, k_cache.scale_inv, v_cache.cache, v_cache.scale_inv)
+
+
+def _table_shape(block_table, seq_lens, what="block_table"):
+    if block_table.dim() != 2 or seq_lens.dim() != 1 or block_table.shape[0] != seq_lens.shape[0]:
+        raise ValueError(f"expected {what} [B, max_blocks] and seq_lens [B]")
+    return block_table.shape
+
+
+def paged_attention_workspace(B, Hq, H, Dh, max_context=0, weights=False, tokens=0, device="cuda"):
+    """Scratch of paged_attention_decode (tokens = 0; max_context = columns of the block table x block size,
+    weights when mass is asked for) or of paged_attention_prefill (tokens = rows of q); None if it needs none."""
+    with torch.cuda.device(device):
+        n = fp8_paged_attention_workspace_size(B, Hq, H, Dh, max_context, weights, tokens)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def paged_attention_decode(q, k_cache, v_cache, block_table, seq_lens, window=0, sinks=0, softmax_scale=None,
+                           mass=None, mass_decay=1.0, out=None, workspace=None):
+    """(out [B, Hq, Dh] bf16, lse [B, Hq] fp32): attention of one new token per sequence, q [B, Hq, Dh], over the
+    paged caches (PagedKVCache of K and of V).  window > 0: only the last `window` positions and the first `sinks`.
+    mass [B, H, ld] fp32: becomes mass_decay * mass + each visible token's attention weight, summed over the query
+    heads of its KV head.  softmax_scale: Dh ** -0.5 unless given."""
+    ld_q = _token_rows(q, "q")
+    B, Hq, Dh = q.shape
+    caches = _kv_pair(k_cache, v_cache)
+    H = k_cache.H
+    if Dh != k_cache.Dh:
+        raise ValueError("q and the caches must have the same head size")
+    nb, mb = _table_shape(block_table, seq_lens)
+    if nb != B or (mass is not None and (mass.dim() != 3 or tuple(mass.shape[:2]) != (B, H))):
+        raise ValueError("q, block_table, seq_lens and mass must be of one batch")
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    o = out if out is not None else torch.empty((B, Hq, Dh), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = paged_attention_workspace(B, Hq, H, Dh, mb * k_cache.block_size, mass is not None, 0, q.device)
+    fp8_paged_attention_decode(q, ld_q, B, Hq, *caches, H, Dh, k_cache.block_size, k_cache.num_blocks, k_cache.fmt,
+                               block_table, seq_lens, mb, window, sinks,
+                               Dh ** -0.5 if softmax_scale is None else softmax_scale, o, lse, mass,
+                               0 if mass is None else mass.shape[2], mass_decay, workspace)
+    return o, lse
+
+
+def paged_attention_prefill(q, q_offsets, k_cache, v_cache, block_table, seq_lens, window=0, sinks=0,
+                            softmax_scale=None, out=None, workspace=None):
+    """(out [T, Hq, Dh] bf16, lse [T, Hq] fp32): causal attention of the rows q_offsets[b] .. q_offsets[b + 1]
+    (int64 [B + 1], device) of q [T, Hq, Dh], the last positions of sequence b, over the paged caches.  Rows that
+    belong to no sequence are not written."""
+    ld_q = _token_rows(q, "q")
+    T, Hq, Dh = q.shape
+    caches = _kv_pair(k_cache, v_cache)
+    H = k_cache.H
+    if Dh != k_cache.Dh:
+        raise ValueError("q and the caches must have the same head size")
+    B, mb = _table_shape(block_table, seq_lens)
+    if q_offsets.dim() != 1 or q_offsets.shape[0] != B + 1:
+        raise ValueError("expected q_offsets [B + 1]")
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    o = out if out is not None else torch.empty((T, Hq, Dh), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    if workspace is None and T:
+        workspace = paged_attention_workspace(B, Hq, H, Dh, tokens=T, device=q.device)
+    fp8_paged_attention_prefill(q, ld_q, T, q_offsets, B, Hq, *caches, H, Dh, k_cache.block_size, k_cache.num_blocks,
+                                k_cache.fmt, block_table, seq_lens, mb, window, sinks,
+                                Dh ** -0.5 if softmax_scale is None else softmax_scale, o, lse, workspace)
+    return o, lse
+
+
+def paged_kv_evict(k_cache, v_cache, block_table, seq_lens, mass, dst_table, budget, sinks=0, recent=0):
+    """(kept [B, H, budget] int32, mass_out like mass, lens_out [B] int32): every sequence cut to its first `sinks`,
+    last `recent` and, of the rest, heaviest tokens by mass [B, H, ld] (`budget` in all), whose rows are copied into
+    the pages of dst_table [B, n], pages that block_table does not use."""
+    caches = _kv_pair(k_cache, v_cache)
+    H, bs = k_cache.H, k_cache.block_size
+    B, mb = _table_shape(block_table, seq_lens)
+    _, db = _table_shape(dst_table, seq_lens, "dst_table")
+    if mass.dim() != 3 or tuple(mass.shape[:2]) != (B, H):
+        raise ValueError("expected mass [B, H, ld]")
+    kept = torch.empty((B, H, max(budget, 0)), dtype=torch.int32, device=mass.device)
+    mass_out = torch.empty_like(mass)
+    lens_out = torch.empty(B, dtype=torch.int32, device=mass.device)
+    fp8_paged_kv_evict(*caches, H, k_cache.Dh, bs, k_cache.num_blocks, block_table, seq_lens, B, mb, mass,
+                       mass.shape[2], dst_table, db, budget, sinks, recent, kept, mass_out, mass.shape[2],
+                       lens_out)
+    return kept, mass_out, lens_out
 
 
 def scale_stats(scales, seg_offsets=None, prev=None, jump_ratio=4.0):

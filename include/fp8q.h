@@ -24,6 +24,10 @@
  *   delayed scaling       fp8_amax_history_update
  *   KV cache              fp8_kv_quant / fp8_kv_dequant (per (b, h) slice),
  *                         fp8_paged_kv_write / fp8_paged_kv_gather (pages)
+ *   attention over pages  fp8_paged_attention_decode (one new token per
+ *                         sequence), fp8_paged_attention_prefill (several),
+ *                         fp8_paged_attention_workspace_size,
+ *                         fp8_paged_kv_evict (by attention weight)
  *   health and errors     fp8_scale_stats, fp8_device_error,
  *                         fp8_status_string
  *
@@ -510,6 +514,131 @@ FP8Q_API fp8_status fp8_paged_kv_gather(const uint8_t *cache, const float *scale
                                int64_t max_blocks, int64_t H, int64_t Dh, int64_t block_size,
                                int64_t num_blocks, int64_t S_out, fp8_format fmt, void *out_bf16,
                                void *stream);
+
+/*
+ * Attention of one new token per sequence over the paged FP8 KV cache, read
+ * in place ([DeepL] §3.1: K and V stored in FP8; the codes are never expanded
+ * in memory).  For sequence b with n = seq_lens[b] cached tokens (its new
+ * token, position n - 1, already written), KV head h and the query heads of
+ * its group (query head i reads KV head i / (Hq / H)):
+ *   k_j = fp32(k_cache[slot_j][h]) * k_scale[slot_j][h],  v_j likewise,
+ *   slot_j = block_table[b][j / block_size] * block_size + j % block_size,
+ *   z_j = softmax_scale * (q . k_j) over the visible positions j,
+ *   out = sum_j exp(z_j - lse) v_j,   lse = log sum_j exp(z_j).
+ * Position j is visible to the query at position p (here n - 1) when j <= p,
+ * its page id lies in [0, num_blocks), and window == 0, j > p - window or
+ * j < sinks: a sliding window of `window` positions (the query's own among
+ * them) plus the first `sinks` positions, which stay visible.  A query that
+ * sees nothing (n == 0) gets out = 0, lse = -inf.  What lies in slots that are
+ * not visible is never read into a result, whatever it is.
+ *   q_bf16      [B, Hq, Dh] bf16, ld_q elements between tokens (a slice of a
+ *               fused projection's output will do).
+ *   k_cache, v_cache [num_blocks, block_size, H, Dh] FP8 of one format,
+ *   k_scale, v_scale [num_blocks, block_size, H] fp32, as written by
+ *               fp8_paged_kv_write.
+ *   block_table [B, max_blocks] int32, seq_lens [B] int32, device; a length
+ *               outside [0, max_blocks * block_size] counts as the nearer end.
+ *   out_bf16    [B, Hq, Dh] bf16, dense.  lse [B, Hq] fp32 or NULL.
+ *   mass        [B, H, ld_mass] fp32 or NULL: the attention weight that each
+ *               cached token received, summed over the query heads of its KV
+ *               head: mass[b][h][j] = mass_decay * mass[b][h][j] + sum of
+ *               exp(z_j - lse), for the visible j < ld_mass; other entries are
+ *               left as they were.  mass_decay == 0 overwrites without
+ *               reading, 1 accumulates (fp8_paged_kv_evict's input).
+ *   workspace   fp8_paged_attention_workspace_size() bytes, 16-byte aligned;
+ *               its contents need no initialisation and nothing is kept in it
+ *               between calls, but calls that may run at the same time (two
+ *               streams, two graphs replayed together) need one each.
+ *   Deterministic: the split over the cache's length depends on the lengths
+ *   and the device only, and its parts are joined in a fixed order.  P and the
+ *   products with V are fp16 tensor-core products with fp32 sums; logits,
+ *   maxima and sums are fp32.
+ *   Shapes: Dh % 16 == 0, 16 <= Dh <= 256, H * Dh <= 8192, Hq % H == 0,
+ *   B <= 65535, num_blocks * block_size < 2^31, window, sinks >= 0,
+ *   softmax_scale and mass_decay finite.
+ *   Errors: FP8_ERR_SHAPE, FP8_ERR_INVALID_ARG (NULL pointer, format, a
+ *   workspace that is too small, a scale that is not finite),
+ *   FP8_ERR_ALIGNMENT (q, out, the caches and the workspace 16 bytes, ld_q a
+ *   multiple of 8).
+ */
+FP8Q_API fp8_status fp8_paged_attention_decode(
+    const void *q_bf16, int64_t ld_q, int64_t B, int64_t Hq, const uint8_t *k_cache, const float *k_scale,
+    const uint8_t *v_cache, const float *v_scale, int64_t H, int64_t Dh, int64_t block_size, int64_t num_blocks,
+    fp8_format fmt, const int32_t *block_table, const int32_t *seq_lens, int64_t max_blocks, int64_t window,
+    int64_t sinks, float softmax_scale, void *out_bf16, float *lse, float *mass, int64_t ld_mass, float mass_decay,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Causal attention of several new tokens per sequence over the paged FP8 KV
+ * cache (a prompt, a chunk of one, a few drafted tokens), the new tokens' K and V
+ * already written.  Rows q_offsets[b] <= t < q_offsets[b + 1] of q are the last
+ * positions of sequence b: row t sits at position
+ *   p = seq_lens[b] - (q_offsets[b + 1] - q_offsets[b]) + (t - q_offsets[b])
+ * and attends by the formulas and the visibility rule of
+ * fp8_paged_attention_decode (a row whose p is negative sees nothing).
+ *   q_bf16    [T, Hq, Dh] bf16, ld_q elements between tokens.
+ *   q_offsets [B + 1] int64, device, non-decreasing, clamped to [0, T] on the
+ *             device; rows before the first and behind the last offset are
+ *             not written.
+ *   out_bf16  [T, Hq, Dh] bf16, dense.  lse [T, Hq] fp32 or NULL.
+ *   The remaining arguments, shapes, errors, determinism and the workspace are
+ *   those of fp8_paged_attention_decode.  T * Hq < 2^31.
+ */
+FP8Q_API fp8_status fp8_paged_attention_prefill(
+    const void *q_bf16, int64_t ld_q, int64_t T, const int64_t *q_offsets, int64_t B, int64_t Hq,
+    const uint8_t *k_cache, const float *k_scale, const uint8_t *v_cache, const float *v_scale, int64_t H, int64_t Dh,
+    int64_t block_size, int64_t num_blocks, fp8_format fmt, const int32_t *block_table, const int32_t *seq_lens,
+    int64_t max_blocks, int64_t window, int64_t sinks, float softmax_scale, void *out_bf16, float *lse,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Workspace of the two attention calls on the current device: pass tokens = 0
+ * for fp8_paged_attention_decode (max_context = max_blocks * block_size and
+ * weights != 0 when mass is asked for), tokens = T for
+ * fp8_paged_attention_prefill (max_context and weights are then ignored).
+ * The size does not grow with B beyond the weights' scratch.
+ */
+FP8Q_API fp8_status fp8_paged_attention_workspace_size(int64_t B, int64_t Hq, int64_t H, int64_t Dh,
+                                                       int64_t max_context, int weights, int64_t tokens,
+                                                       size_t *bytes);
+
+/*
+ * Eviction from the paged FP8 KV cache by accumulated attention weight.  For
+ * each sequence b (n = seq_lens[b] tokens) and KV head h:
+ *   n <= budget : every token is kept;
+ *   n >  budget : the first `sinks`, the last `recent`, and of the tokens
+ *                 between them the budget - sinks - recent with the largest
+ *                 mass (equal masses: the lower position; NaN counts as -inf;
+ *                 a position at or past ld_mass has mass 0).
+ * The kept tokens' rows (K and V codes, bit for bit, and their scales) are
+ * copied in ascending order of position to positions 0, 1, ... of the pages of
+ * dst_table[b], each head by its own choice; attention without further
+ * position input does not depend on which position a row sits at.
+ *   k_cache .. v_scale  the cache, read through block_table and written
+ *               through dst_table.  The destination pages must not be source
+ *               pages of this call and must be distinct (otherwise which row
+ *               a slot ends up with is unspecified); source pages are left as
+ *               they were, so pages shared with other sequences stay valid.
+ *   block_table [B, max_blocks], dst_table [B, dst_max_blocks] int32.  A row
+ *               whose source page id lies outside [0, num_blocks) is copied as
+ *               zeros; one whose destination does is not copied.
+ *   seq_lens    [B] int32, as in fp8_paged_attention_decode.
+ *   mass        [B, H, ld_mass] fp32.
+ *   kept        [B, H, budget] int32: the kept positions, ascending, then -1.
+ *   mass_out    [B, H, ld_out] fp32, not overlapping mass: the kept tokens'
+ *               masses (those of positions below ld_out), then zeros.
+ *   lens_out    [B] int32: min(n, budget); may be seq_lens itself.
+ *   Shapes: Dh % 8 == 0, H * Dh <= 8192, B <= 65535, budget >= 1, sinks and
+ *   recent >= 0, sinks + recent <= budget, num_blocks * block_size < 2^31.
+ *   Errors: FP8_ERR_SHAPE, FP8_ERR_INVALID_ARG (NULL pointer),
+ *   FP8_ERR_ALIGNMENT (the caches: 16 bytes).
+ */
+FP8Q_API fp8_status fp8_paged_kv_evict(uint8_t *k_cache, float *k_scale, uint8_t *v_cache, float *v_scale, int64_t H,
+                                       int64_t Dh, int64_t block_size, int64_t num_blocks, const int32_t *block_table,
+                                       const int32_t *seq_lens, int64_t B, int64_t max_blocks, const float *mass,
+                                       int64_t ld_mass, const int32_t *dst_table, int64_t dst_max_blocks,
+                                       int64_t budget, int64_t sinks, int64_t recent, int32_t *kept, float *mass_out,
+                                       int64_t ld_out, int32_t *lens_out, void *stream);
 
 /*
  * Health check of scale factors ([DeepL] §6.2: report the min / max / mean of
