@@ -12,6 +12,9 @@ namespace {
 using namespace fp8q;
 
 constexpr int kPagedMaxRow = 8192;   // H * Dh per token, the cache's own limit
+// max_blocks * block_size: positions, and the ends of the tiles that hold
+// them, stay below 2^31
+constexpr int64_t kPagedMaxContext = 0x7FFF0000ll;
 
 // n / d for 0 <= n < 2^31, d fixed for a launch: multiply and shift (Granlund
 // and Montgomery's round-up form), because the table lookup of every position
@@ -34,7 +37,7 @@ struct PagedView {
     const int32_t *table, *lens;
     int64_t max_blocks;
     FastDiv bs;
-    int num_blocks, H, Dh, cap;   // cap = max_blocks * block_size, at most 2^31 - 1
+    int num_blocks, H, Dh, cap;   // cap = max_blocks * block_size, at most kPagedMaxContext
     int window, sinks;            // window == 0: none
 
     __device__ __forceinline__ int length(int64_t b) const {
@@ -76,7 +79,7 @@ inline PagedView make_paged_view(const uint8_t *kc, const float *ks, const uint8
     v.bs = make_fastdiv((uint32_t)block_size);
     v.num_blocks = (int)num_blocks; v.H = (int)H; v.Dh = (int)Dh;
     const int64_t lim = 0x7FFFFFFFll;
-    v.cap = (int)(max_blocks > lim / block_size ? lim : max_blocks * block_size);
+    v.cap = (int)(max_blocks * block_size);
     v.window = (int)(window > lim ? 0 : window);   // a window of 2^31 or more hides nothing
     v.sinks = (int)(sinks > lim ? lim : sinks);
     return v;

@@ -1,0 +1,814 @@
+// paged_decode.cu -- attention of one new token per sequence over the paged
+// FP8 KV cache.
+//
+// Per KV head the work is S^T = K Q^T (positions x query heads of the group),
+// a softmax over the positions and O^T = V^T P^T.  Every K and V byte is used
+// once per group of query heads, so the kernel is bound by reading the cache:
+// what it has to reach is the HBM rate, and what stands against that is the
+// instructions spent on each byte.  Hence:
+//   * a warp owns one KV head and 16 positions at a time, copied by cp.async
+//     (16 bytes a lane, a few tiles ahead) into shared memory slots that the
+//     same lane reads back, so no barrier stands between copy and use;
+//   * the copied bytes are matrix fragments as they lie: any permutation of
+//     the head elements is allowed in K Q^T when Q is permuted alike (lane t of
+//     a row takes whole 16-byte chunks), and any permutation of V's columns
+//     only permutes the rows of O^T, so nothing is transposed but V's pairs of
+//     positions (one byte permute per four codes);
+//   * E4M3 and E5M2 codes are exact in fp16 (one conversion per two codes), so
+//     the products run as mma.m16n8k16 on fp16 with fp32 sums (N = 8 query
+//     heads fits a group; the tensor rate is not the bound).  The rows' scales
+//     multiply the logits and the weights, in fp32, per position;
+//   * Q's rows are brought to [2^14, 2^15) by a power of two before they become
+//     fp16, which is then exact for every element above 2^-24 of the row's
+//     largest; the weights times V's scales are normalised by a running power
+//     of two, so that fp16 holds them to 2^-11 down to 2^-22 of the largest;
+//   * the maximum is only moved when a logit passes it by 2^6 (one vote per
+//     tile instead of shuffles); weights stay below 2^6, far inside fp16.
+//
+// Split: the tiles of all (sequence, block of heads) are laid end to end and
+// every CTA takes an equal, contiguous run of them, whatever the lengths (they
+// are only known on the device).  A CTA that covers all of a row's tiles
+// writes its result; otherwise it leaves (O, max, sum) in the workspace and
+// k_decode_join adds the parts in the order of the CTAs.  At most two parts
+// per CTA, so the workspace does not grow with the batch.
+#include <algorithm>
+#include <atomic>
+
+#include "paged_attn.cuh"
+
+using namespace fp8q;
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kTile = 16;                    // positions per warp and step
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNoMax = -3.0e38f;           // before the first logit; below every finite logit that matters
+constexpr float kLazy = 6.0f;                // log2 of how far a logit may pass the maximum in use
+
+struct DecodeArgs {
+    const __nv_bfloat16 *q;
+    int64_t ld_q;
+    int B, G, GC, HB;        // query heads per KV head; chunks of them; (virtual) heads per CTA
+    float scale;
+    __nv_bfloat16 *out;
+    float *lse;              // [B, Hq]
+    float *part;             // two parts per CTA
+    float *logits;           // weights' scratch [B, H * GC, vis_max, 8 * NT] (log2 units), or nullptr
+    int64_t vis_max;
+    float *mass;
+    int64_t ld_mass;
+    float decay;
+};
+
+template <int DH, int NT>
+struct Cfg {
+    static constexpr int STAGE = 32 * DH + 128 + 16;     // K, V, 32 scales, the mask of live positions
+    static constexpr int MIN_CTAS = (DH <= 128 && NT == 1) ? 2 : 1;
+    static constexpr int STAGES = DH == 64 ? 5 : DH == 128 ? (NT == 1 ? 3 : 5) : 3;
+    static constexpr size_t SMEM = (size_t)kWarps * STAGES * STAGE;
+    static constexpr int COLS = 8 * NT;                  // query heads per chunk
+    static_assert(STAGES * STAGE >= COLS * DH * 4, "the warps' results are merged in the pipeline's memory");
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// copies BYTES, or writes zeros when !live
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool live) {
+    const int n = live ? BYTES : 0;
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n)
+                     : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+    return v;
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t to_f16x2(uint32_t c) {   // the two codes in the low half (exact)
+    uint32_t h;
+    if (FMT == FP8_E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+    else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+    return h;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 0 at -inf and below 2^-126
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+// 2^e for -126 <= e <= 127; infinity at 128
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Visible positions of the one query of sequence b: index i < sinks is
+// position i, the others follow from `begin`.
+struct Visible {
+    int begin, sinks, count;
+    __device__ __forceinline__ int position(int i) const { return i < sinks ? i : begin + (i - sinks); }
+};
+__device__ __forceinline__ Visible visible_of(const PagedView &pv, int64_t b) {
+    const int n = pv.length(b);
+    Visible v;
+    v.begin = pv.window_begin(n - 1);
+    v.sinks = min(pv.sinks, v.begin);
+    v.count = n - v.begin + v.sinks;
+    return v;
+}
+
+// Tiles laid end to end: rows (b, hb) with b slowest; nt_b tiles in each row of
+// sequence b.
+__device__ __forceinline__ int tiles_of(const PagedView &pv, int64_t b, int per_tile) {
+    return (visible_of(pv, b).count + per_tile - 1) / per_tile;
+}
+__device__ int64_t block_scan(int64_t v, int64_t *buf, int64_t *total) {   // exclusive
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) buf[warp] = x;
+    __syncthreads();
+    int64_t base = 0, all = 0;
+    for (int w = 0; w < nw; ++w) {
+        if (w < warp) base += buf[w];
+        all += buf[w];
+    }
+    *total = all;
+    return base + x - v;
+}
+// Block-wide: the tiles of all sequences, and those of the sequences before `b`.
+__device__ void count_tiles(const PagedView &pv, int B, int per_tile, int rows, int b, int64_t *buf, int64_t *total,
+                            int64_t *before) {
+    int64_t all = 0, pre = 0;
+    for (int i = threadIdx.x; i < B; i += blockDim.x) {
+        const int64_t n = (int64_t)tiles_of(pv, i, per_tile) * rows;
+        all += n;
+        if (i < b) pre += n;
+    }
+    block_scan(pre, buf, before);
+    block_scan(all, buf, total);
+}
+// First tile of CTA c of n when `total` tiles are dealt out evenly.
+__device__ __forceinline__ int64_t deal(int64_t total, int64_t n, int64_t c) { return total * c / n; }
+
+template <int FMT, int DH, int NT>
+__global__ void __launch_bounds__(kWarps * 32, Cfg<DH, NT>::MIN_CTAS)
+k_decode(const PagedView pv, const DecodeArgs a) {
+    using C = Cfg<DH, NT>;
+    constexpr int KC = DH / 64;              // 16-byte chunks of a K row per lane
+    constexpr int VB = DH / 8;               // V bytes of a position per lane
+    constexpr int KS = DH / 16;              // k steps of K Q^T
+    constexpr int MI = DH / 16;              // row blocks of O^T
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int64_t scan_buf[kWarps], s_before;
+    __shared__ int s_b;
+    __shared__ float s_m[kWarps][C::COLS], s_l[kWarps][C::COLS];
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int WT = kWarps / a.HB;            // warps that share a head, a tile of positions each
+    const int hw = warp / WT, wt = warp % WT;
+    const int VH = pv.H * a.GC, rows = VH / a.HB, per_tile = kTile * WT;
+    pdl_wait();
+    pdl_trigger();
+
+    // the first of this CTA's tiles: its sequence, and the tiles before that
+    int64_t total, unused;
+    int64_t mine = 0;
+    if (a.B <= kWarps * 32) {
+        if (threadIdx.x < a.B) mine = (int64_t)tiles_of(pv, threadIdx.x, per_tile) * rows;
+    } else {
+        count_tiles(pv, a.B, per_tile, rows, 0, scan_buf, &total, &unused);
+    }
+    int64_t pre = 0;
+    if (a.B <= kWarps * 32) pre = block_scan(mine, scan_buf, &total);
+    const int64_t ncta = min((int64_t)gridDim.x, total);
+    if ((int64_t)blockIdx.x >= ncta) return;
+    int64_t at = deal(total, ncta, blockIdx.x);
+    const int64_t end = deal(total, ncta, blockIdx.x + 1);
+    for (int64_t b0 = 0, base = 0;; b0 += kWarps * 32) {
+        if (a.B > kWarps * 32) {
+            const int64_t bb = b0 + threadIdx.x;
+            mine = bb < a.B ? (int64_t)tiles_of(pv, bb, per_tile) * rows : 0;
+            int64_t all;
+            pre = base + block_scan(mine, scan_buf, &all);
+            base += all;
+        } else {
+            base = total;
+        }
+        if (at >= pre && at < pre + mine) {
+            s_b = (int)(b0 + threadIdx.x);
+            s_before = pre;
+        }
+        if (at < base) break;                 // at < total: some round ends here
+    }
+    __syncthreads();
+    int b = s_b;
+    Visible vis = visible_of(pv, b);
+    int nt = (vis.count + per_tile - 1) / per_tile;
+    int row = (int)((at - s_before) / nt), tile = (int)((at - s_before) % nt);
+
+    const uint32_t sm = smem_addr(smem) + (uint32_t)(warp * C::STAGES * C::STAGE);
+    const int64_t row_bytes = (int64_t)pv.H * pv.Dh;
+
+    while (true) {
+        const int tile_end = (int)min((int64_t)nt, tile + (end - at));
+        const int vh = row * a.HB + hw, h = vh / a.GC, chunk = vh % a.GC;
+
+        // ---- Q: this warp's chunk of the group, as fp16 fragments
+        uint32_t qf[NT][KS][2];
+        float cf[NT][2];                      // logit factor (log2 units) of columns 2t, 2t + 1
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            const int gi = chunk * C::COLS + x * 8 + g;
+            const __nv_bfloat16 *qp = a.q + (int64_t)b * a.ld_q + (int64_t)(h * a.G + gi) * pv.Dh;
+            uint4 w[KC][2];
+            uint32_t mx = 0;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const int d0 = 16 * (t + 4 * c);
+                const bool live = gi < a.G && d0 < pv.Dh;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    w[c][e] = live ? *reinterpret_cast<const uint4 *>(qp + d0 + 8 * e) : make_uint4(0, 0, 0, 0);
+                    uint32_t bad = 0;
+                    mx = amax_exact8(mx, w[c][e], bad);       // finite elements only
+                }
+            }
+            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+            const int ex = max((int)(mx >> 7), 14) - 127;     // exponent of the row's largest, at least 2^-113
+            const float up = pow2i(14 - ex);
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const uint32_t ww[8] = {w[c][0].x, w[c][0].y, w[c][0].z, w[c][0].w,
+                                        w[c][1].x, w[c][1].y, w[c][1].z, w[c][1].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        qf[x][c * 4 + i][e] = pack_f16x2(bf_lo(ww[2 * i + e]) * up, bf_hi(ww[2 * i + e]) * up);
+            }
+            const float f = a.scale * kLog2e * pow2i(ex) * 0x1p-14f;
+            cf[x][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);
+            cf[x][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
+        }
+
+        float o[NT][MI][4], m[NT][2], l[NT][2], vscale = 1.0f, vcap = 0.0f;
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[x][i][e] = 0.0f;
+            m[x][0] = m[x][1] = kNoMax;
+            l[x][0] = l[x][1] = 0.0f;
+        }
+
+        const uint8_t *kh = pv.kc + (int64_t)h * pv.Dh, *vhp = pv.vc + (int64_t)h * pv.Dh;
+        const int ntile = tile_end - tile;
+        // slot of this lane's position (lanes 16.. repeat 0..15) of the k-th tile
+        auto slot_of = [&](int k) {
+            const int i = ((tile + k) * WT + wt) * kTile + (lane & 15);
+            return k < ntile && i < vis.count ? pv.slot(b, vis.position(i)) : -1;
+        };
+        int next_slot = slot_of(0);
+        auto issue = [&](int k) {             // copies of the k-th tile
+            if (k < ntile) {
+                const uint32_t st = sm + (uint32_t)(k % C::STAGES) * C::STAGE;
+                const int slot = next_slot;
+                const uint32_t live = __ballot_sync(0xFFFFFFFFu, slot >= 0);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int s = __shfl_sync(0xFFFFFFFFu, slot, g + 8 * r);
+                    const uint8_t *src = kh + (int64_t)max(s, 0) * row_bytes + 16 * t;
+#pragma unroll
+                    for (int c = 0; c < KC; ++c)
+                        cp_async<16>(st + (uint32_t)(((r * KC + c) * 32 + lane) * 16), src + 64 * c,
+                                     s >= 0 && 16 * (t + 4 * c) < pv.Dh);
+                }
+                const uint32_t sv = st + 16 * DH;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int s = __shfl_sync(0xFFFFFFFFu, slot, 2 * t + (e & 1) + 4 * (e & 2));
+                    const uint8_t *src = vhp + (int64_t)max(s, 0) * row_bytes + VB * g;
+                    if constexpr (VB == 8) {
+                        cp_async<8>(sv + (uint32_t)((e * 32 + lane) * 8), src, s >= 0 && 8 * g < pv.Dh);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < VB / 16; ++c)
+                            cp_async<16>(sv + (uint32_t)(((e * (VB / 16) + c) * 32 + lane) * 16), src + 16 * c,
+                                         s >= 0 && VB * g + 16 * c < pv.Dh);
+                    }
+                }
+                const float *sp = (lane < 16 ? pv.ks : pv.vs) + (int64_t)max(slot, 0) * pv.H + h;
+                cp_async<4>(st + 32 * DH + 4 * lane, sp, slot >= 0);
+                if (lane == 0)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + 32 * DH + 128), "r"(live) : "memory");
+                next_slot = slot_of(k + 1);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        for (int k = 0; k < C::STAGES - 1; ++k) issue(k);
+
+        for (int k = 0; k < ntile; ++k) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::STAGES - 2) : "memory");
+            __syncwarp();                     // the other lanes' scales; and tile k - 1 is read by all
+            issue(k + C::STAGES - 1);
+            const uint32_t st = sm + (uint32_t)(k % C::STAGES) * C::STAGE, sc = st + 32 * DH;
+            uint32_t live;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(live) : "r"(sc + 128));
+
+            // ---- S^T = K Q^T
+            float s[NT][4];
+#pragma unroll
+            for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const uint4 k0 = lds128(st + (uint32_t)((c * 32 + lane) * 16));
+                const uint4 k1 = lds128(st + (uint32_t)(((KC + c) * 32 + lane) * 16));
+                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a0 = to_f16x2<FMT>(w0[i]), a2 = to_f16x2<FMT>(w0[i] >> 16);
+                    const uint32_t a1 = to_f16x2<FMT>(w1[i]), a3 = to_f16x2<FMT>(w1[i] >> 16);
+#pragma unroll
+                    for (int x = 0; x < NT; ++x) mma16816(s[x], a0, a1, a2, a3, qf[x][c * 4 + i][0], qf[x][c * 4 + i][1]);
+                }
+            }
+            // ---- logits in log2 units; what is not visible becomes -inf
+            const float dk0 = lds_f(sc + 4 * g), dk1 = lds_f(sc + 4 * (g + 8));
+            const float dv0 = lds_f(sc + 4 * (g + 16)), dv1 = lds_f(sc + 4 * (g + 24));
+            bool up = false;
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    s[x][e] *= dk0 * cf[x][e];
+                    s[x][2 + e] *= dk1 * cf[x][e];
+                }
+                if (live != 0xFFFFFFFFu) {
+                    if (!((live >> g) & 1u)) s[x][0] = s[x][1] = -INFINITY;
+                    if (!((live >> (g + 8)) & 1u)) s[x][2] = s[x][3] = -INFINITY;
+                }
+                up |= fmaxf(s[x][0], s[x][2]) > m[x][0] + kLazy || fmaxf(s[x][1], s[x][3]) > m[x][1] + kLazy;
+            }
+            if (a.logits) {
+                const int i0 = ((tile + k) * WT + wt) * kTile;
+                float *lp = a.logits + (((int64_t)b * VH + vh) * a.vis_max + i0) * C::COLS + 2 * t;
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+                    if (i0 + g < vis.count)
+                        *reinterpret_cast<float2 *>(lp + g * C::COLS + 8 * x) = make_float2(s[x][0], s[x][1]);
+                    if (i0 + g + 8 < vis.count)
+                        *reinterpret_cast<float2 *>(lp + (g + 8) * C::COLS + 8 * x) = make_float2(s[x][2], s[x][3]);
+                }
+            }
+            if (__any_sync(0xFFFFFFFFu, up)) {
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(m[x][e], fmaxf(s[x][e], s[x][2 + e]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+                        const float al = exp2_fast(m[x][e] - mx);
+                        m[x][e] = mx;
+                        l[x][e] *= al;
+#pragma unroll
+                        for (int i = 0; i < MI; ++i) {
+                            o[x][i][e] *= al;
+                            o[x][i][2 + e] *= al;
+                        }
+                    }
+            }
+            // ---- the power of two that V's scales are held against
+            const float dmax = fmaxf(fabsf(dv0), fabsf(dv1));
+            if (__any_sync(0xFFFFFFFFu, dmax > vcap && dmax < INFINITY)) {
+                const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, dmax < INFINITY ? __float_as_uint(dmax) : 0u);
+                const int ex = max((int)(bits >> 23) - 127, -100);   // dmax < 2^(ex + 1)
+                const float vs = pow2i(8 - ex), r = vcap > 0.0f ? vs / vscale : 1.0f;
+                vscale = vs;                                                   // dv * vscale < 2^9
+                vcap = pow2i(ex + 1);
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+#pragma unroll
+                    for (int i = 0; i < MI; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[x][i][e] *= r;
+            }
+            const float f0 = dv0 * vscale, f1 = dv1 * vscale;
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                const float p0 = exp2_fast(s[x][0] - m[x][0]), p1 = exp2_fast(s[x][1] - m[x][1]);
+                const float p2 = exp2_fast(s[x][2] - m[x][0]), p3 = exp2_fast(s[x][3] - m[x][1]);
+                l[x][0] += p0 + p2;
+                l[x][1] += p1 + p3;
+                pb[x][0] = transpose8x8(pack_f16x2(p0 * f0, p1 * f0));
+                pb[x][1] = transpose8x8(pack_f16x2(p2 * f1, p3 * f1));
+            }
+            // ---- O^T += V^T P^T
+            const uint32_t sv = st + 16 * DH;
+#pragma unroll
+            for (int c = 0; c < (VB + 15) / 16; ++c) {
+                uint32_t v[4][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (VB == 8) {
+                        const uint2 w = lds64(sv + (uint32_t)((e * 32 + lane) * 8));
+                        v[e][0] = w.x; v[e][1] = w.y;
+                    } else {
+                        const uint4 w = lds128(sv + (uint32_t)(((e * (VB / 16) + c) * 32 + lane) * 16));
+                        v[e][0] = w.x; v[e][1] = w.y; v[e][2] = w.z; v[e][3] = w.w;
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < (VB == 8 ? 2 : 4); ++w)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint32_t sel = hf ? 0x7362u : 0x5140u;
+                        const uint32_t xx = __byte_perm(v[0][w], v[1][w], sel), yy = __byte_perm(v[2][w], v[3][w], sel);
+                        const uint32_t a0 = to_f16x2<FMT>(xx), a1 = to_f16x2<FMT>(xx >> 16);
+                        const uint32_t a2 = to_f16x2<FMT>(yy), a3 = to_f16x2<FMT>(yy >> 16);
+#pragma unroll
+                        for (int x = 0; x < NT; ++x)
+                            mma16816(o[x][c * 8 + w * 2 + hf], a0, a1, a2, a3, pb[x][0], pb[x][1]);
+                    }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+
+        // ---- this run of tiles is done: result, or a part of one
+        const float inv = 1.0f / vscale;
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v = l[x][e];
+                v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+                v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+                v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+                l[x][e] = v;
+            }
+        const bool whole = tile == 0 && tile_end == nt;
+        float *part = a.part + ((int64_t)blockIdx.x * 2 + (tile == 0 ? 1 : 0)) * a.HB * C::COLS * (DH + 2);
+        // column c of head hw: DH sums, then (max, sum) behind all columns' sums
+        float *part_ml = part + (int64_t)a.HB * C::COLS * DH;
+        if (WT == 1) {
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int col = 8 * x + 2 * t + e, gi = chunk * C::COLS + col;
+                    if (gi >= a.G) continue;
+                    if (whole) {
+                        const float r = l[x][e] == 0.0f ? 0.0f : inv / l[x][e];
+                        const int64_t orow = (int64_t)b * pv.H * a.G + h * a.G + gi;
+                        if (g == 0) a.lse[orow] = l[x][e] == 0.0f ? -INFINITY : (m[x][e] + log2f(l[x][e])) * kLn2;
+                        __nv_bfloat16 *op = a.out + orow * pv.Dh + VB * g;
+#pragma unroll
+                        for (int c = 0; c < VB / 8; ++c)
+                            if (VB * g + 8 * c < pv.Dh) {
+                                uint4 w;
+                                w.x = pack_bf16x2(o[x][4 * c][e] * r, o[x][4 * c][2 + e] * r);
+                                w.y = pack_bf16x2(o[x][4 * c + 1][e] * r, o[x][4 * c + 1][2 + e] * r);
+                                w.z = pack_bf16x2(o[x][4 * c + 2][e] * r, o[x][4 * c + 2][2 + e] * r);
+                                w.w = pack_bf16x2(o[x][4 * c + 3][e] * r, o[x][4 * c + 3][2 + e] * r);
+                                *reinterpret_cast<uint4 *>(op + 8 * c) = w;
+                            }
+                    } else {
+                        const int pc = hw * C::COLS + col;
+                        if (g == 0) *reinterpret_cast<float2 *>(part_ml + 2 * pc) = make_float2(m[x][e], l[x][e]);
+                        float *pp = part + (int64_t)pc * DH + VB * g;
+#pragma unroll
+                        for (int i = 0; i < MI; i += 2)
+                            *reinterpret_cast<float4 *>(pp + 2 * i) =
+                                make_float4(o[x][i][e] * inv, o[x][i][2 + e] * inv, o[x][i + 1][e] * inv,
+                                            o[x][i + 1][2 + e] * inv);
+                    }
+                }
+        } else {
+            __syncthreads();                  // every warp's copies have landed and been read
+            float *mine = reinterpret_cast<float *>(smem + (size_t)warp * C::STAGES * C::STAGE);
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int col = 8 * x + 2 * t + e;
+                    if (g == 0) {
+                        s_m[warp][col] = m[x][e];
+                        s_l[warp][col] = l[x][e];
+                    }
+#pragma unroll
+                    for (int i = 0; i < MI; ++i)
+                        *reinterpret_cast<float2 *>(mine + col * DH + VB * g + 2 * i) =
+                            make_float2(o[x][i][e] * inv, o[x][i][2 + e] * inv);
+                }
+            __syncthreads();
+            // four elements per thread and step
+            for (int idx = threadIdx.x; idx < a.HB * C::COLS * (DH / 4); idx += kWarps * 32) {
+                const int d = idx % (DH / 4) * 4, pc = idx / (DH / 4), col = pc % C::COLS, hh = pc / C::COLS;
+                const int vh2 = row * a.HB + hh, gi = vh2 % a.GC * C::COLS + col;
+                if (gi >= a.G) continue;
+                float mx = kNoMax;
+                for (int w = 0; w < WT; ++w) mx = fmaxf(mx, s_m[hh * WT + w][col]);
+                float sum = 0.0f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int w = 0; w < WT; ++w) {
+                    const float al = exp2_fast(s_m[hh * WT + w][col] - mx);
+                    const float4 v = *reinterpret_cast<const float4 *>(
+                        smem + (size_t)(hh * WT + w) * C::STAGES * C::STAGE + (size_t)(col * DH + d) * 4);
+                    sum = fmaf(s_l[hh * WT + w][col], al, sum);
+                    acc.x = fmaf(v.x, al, acc.x); acc.y = fmaf(v.y, al, acc.y);
+                    acc.z = fmaf(v.z, al, acc.z); acc.w = fmaf(v.w, al, acc.w);
+                }
+                if (whole) {
+                    const int64_t orow = (int64_t)b * pv.H * a.G + vh2 / a.GC * a.G + gi;
+                    const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    if (d == 0) a.lse[orow] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+                    if (d < pv.Dh)
+                        *reinterpret_cast<uint2 *>(a.out + orow * pv.Dh + d) =
+                            make_uint2(pack_bf16x2(acc.x * r, acc.y * r), pack_bf16x2(acc.z * r, acc.w * r));
+                } else {
+                    if (d == 0) *reinterpret_cast<float2 *>(part_ml + 2 * pc) = make_float2(mx, sum);
+                    *reinterpret_cast<float4 *>(part + (int64_t)pc * DH + d) = acc;
+                }
+            }
+            __syncthreads();                  // before the next run's copies
+        }
+
+        at += tile_end - tile;
+        if (at >= end) break;
+        tile = 0;
+        if (++row == rows) {
+            row = 0;
+            do {
+                ++b;                          // at < end <= total: another sequence with tiles follows
+                vis = visible_of(pv, b);
+            } while (vis.count == 0);
+            nt = (vis.count + per_tile - 1) / per_tile;
+        }
+    }
+}
+
+// Joins the parts of the rows that more than one CTA worked on, and writes the
+// results of queries that see nothing.  One CTA per (sequence, query head):
+// a warp per part, a lane per DH / 32 elements.
+template <int DH, int COLS>
+__global__ void __launch_bounds__(128)
+k_decode_join(const PagedView pv, const DecodeArgs a, int64_t grid) {
+    constexpr int E = DH / 32;
+    __shared__ int64_t scan_buf[4];
+    __shared__ float s_acc[4][DH], s_ml[4][2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int Hq = pv.H * a.G, b = (int)(blockIdx.x / Hq), hq = (int)(blockIdx.x % Hq), h = hq / a.G, gi = hq % a.G;
+    const int WT = kWarps / a.HB, VH = pv.H * a.GC, rows = VH / a.HB, per_tile = kTile * WT;
+    const int vh = h * a.GC + gi / COLS, row = vh / a.HB, pc = (vh % a.HB) * COLS + gi % COLS;
+    const int64_t orow = (int64_t)b * Hq + hq;
+    pdl_wait();
+    const int nt = tiles_of(pv, b, per_tile);
+    if (nt == 0) {
+        for (int d = threadIdx.x; d < pv.Dh; d += 128) a.out[orow * pv.Dh + d] = __float2bfloat16(0.0f);
+        if (threadIdx.x == 0) a.lse[orow] = -INFINITY;
+        return;
+    }
+    int64_t total, before;
+    count_tiles(pv, a.B, per_tile, rows, b, scan_buf, &total, &before);
+    const int64_t ncta = min(grid, total);
+    const int64_t first = before + (int64_t)row * nt, last = first + nt - 1;
+    // CTA c holds the tiles [total * c / ncta, total * (c + 1) / ncta): the one with tile x is the largest c
+    // with total * c / ncta <= x, that is c <= (x * ncta + ncta - 1) / total
+    const int64_t c0 = (first * ncta + ncta - 1) / total, c1 = (last * ncta + ncta - 1) / total;
+    if (c0 == c1) return;
+    const int64_t stride = (int64_t)a.HB * COLS * (DH + 2), ml = (int64_t)a.HB * COLS * DH + 2 * pc;
+    // the row's tile 0 is in c0, whose part is the second of its two; the others' is their first
+    auto part = [&](int64_t c) { return a.part + (2 * c + (c == c0 ? 1 : 0)) * stride; };
+    float mx = kNoMax, sum = 0.0f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    for (int64_t c = c0 + warp; c <= c1; c += 4) {
+        const float *p = part(c);
+        const float2 v = *reinterpret_cast<const float2 *>(p + ml);
+        const float nm = fmaxf(mx, v.x), al = exp2_fast(mx - nm), be = exp2_fast(v.x - nm);
+        mx = nm;
+        sum = sum * al + v.y * be;
+        const float *o = p + (int64_t)pc * DH + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = acc[e] * al + o[e] * be;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+    if (lane == 0) {
+        s_ml[warp][0] = mx;
+        s_ml[warp][1] = sum;
+    }
+    __syncthreads();
+    mx = fmaxf(fmaxf(s_ml[0][0], s_ml[1][0]), fmaxf(s_ml[2][0], s_ml[3][0]));
+    float al[4];
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        al[w] = exp2_fast(s_ml[w][0] - mx);
+        sum = fmaf(s_ml[w][1], al[w], sum);
+    }
+    const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
+    for (int d = threadIdx.x; d < pv.Dh; d += 128) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v = fmaf(s_acc[w][d], al[w], v);
+        a.out[orow * pv.Dh + d] = __float2bfloat16(v * r);
+    }
+    if (threadIdx.x == 0) a.lse[orow] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+}
+
+// mass of the visible positions from the logits and the joined lse.  One
+// thread per (sequence, KV head, visible index); the heads of the group in order.
+template <int COLS>
+__global__ void __launch_bounds__(256)
+k_decode_mass(const PagedView pv, const DecodeArgs a) {
+    const int b = (int)blockIdx.z, h = (int)blockIdx.y, VH = pv.H * a.GC;
+    pdl_wait();
+    const Visible vis = visible_of(pv, b);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < vis.count; i += (int64_t)gridDim.x * 256) {
+        const int j = vis.position((int)i);
+        if (j >= a.ld_mass || pv.slot(b, j) < 0) continue;
+        float sum = 0.0f;
+        for (int c = 0; c < a.GC; ++c) {
+            const float *lp = a.logits + (((int64_t)b * VH + h * a.GC + c) * a.vis_max + i) * COLS;
+            const float *ls = a.lse + (int64_t)b * pv.H * a.G + h * a.G + c * COLS;
+            for (int e = 0; e < COLS && c * COLS + e < a.G; ++e) sum += exp2_fast(lp[e] - ls[e] * kLog2e);
+        }
+        float *o = a.mass + ((int64_t)b * pv.H + h) * a.ld_mass + j;
+        *o = a.decay == 0.0f ? sum : a.decay * *o + sum;
+    }
+}
+
+}  // namespace
+
+using namespace fp8q_host;
+
+namespace {
+
+struct DecodePlan {
+    int DH, NT, G, GC, HB, ctas, sms;
+    size_t part_bytes, lse_bytes, logit_bytes;
+    size_t total() const { return part_bytes + lse_bytes + logit_bytes; }
+};
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Groups of up to 8 query heads take one column block, larger ones two (16
+// heads per pass over K and V; a head size of 256 has registers for one).
+// Eight warps share out the largest power of two of heads that divides their
+// number, so that no warp is idle.
+DecodePlan decode_plan(int64_t B, int64_t Hq, int64_t H, int64_t Dh, int64_t max_context, bool weights, int sms) {
+    DecodePlan p;
+    p.G = (int)(Hq / H);
+    p.DH = Dh <= 64 ? 64 : Dh <= 128 ? 128 : 256;
+    p.NT = p.G > 8 && p.DH <= 128 ? 2 : 1;
+    p.GC = (p.G + 8 * p.NT - 1) / (8 * p.NT);
+    const int64_t VH = H * p.GC;
+    p.HB = VH % 8 == 0 ? 8 : VH % 4 == 0 ? 4 : VH % 2 == 0 ? 2 : 1;
+    p.sms = sms;
+    p.ctas = sms * (p.DH <= 128 && p.NT == 1 ? 2 : 1);
+    p.part_bytes = round256((size_t)p.ctas * 2 * p.HB * 8 * p.NT * (p.DH + 2) * 4);
+    p.lse_bytes = round256((size_t)(B * Hq) * 4);
+    p.logit_bytes = weights ? round256((size_t)(B * VH) * (size_t)max_context * 8 * p.NT * 4) : 0;
+    return p;
+}
+
+// Dynamic shared memory above 48 KiB is granted per kernel and device, once.
+template <typename K>
+cudaError_t grant_smem(K kernel, size_t bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);     // check_device() admits ordinals below 64
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+template <int FMT, int DH, int NT>
+cudaError_t launch_decode(const PagedView &pv, const DecodeArgs &a, const DecodePlan &p, cudaStream_t s) {
+    using C = Cfg<DH, NT>;
+    static std::atomic<uint64_t> granted{0};
+    cudaError_t e = grant_smem(k_decode<FMT, DH, NT>, C::SMEM, granted);
+    if (e != cudaSuccess) return e;
+    e = pdl_launch(k_decode<FMT, DH, NT>, dim3(p.ctas), dim3(kWarps * 32), C::SMEM, s, pv, a);
+    if (e != cudaSuccess) return e;
+    e = pdl_launch(k_decode_join<DH, C::COLS>, dim3((unsigned)(a.B * (int64_t)pv.H * a.G)), dim3(128), 0, s, pv, a,
+                   (int64_t)p.ctas);
+    if (e != cudaSuccess || !a.logits) return e;
+    // eight CTAs per SM in all, or one per (sequence, head) where there are more of those
+    const int64_t pairs = (int64_t)a.B * pv.H, want = std::max<int64_t>(1, 8 * (int64_t)p.sms / pairs);
+    const unsigned steps = (unsigned)std::min<int64_t>((a.vis_max + 255) / 256, want);
+    return pdl_launch(k_decode_mass<C::COLS>, dim3(std::max(steps, 1u), pv.H, a.B), dim3(256), 0, s, pv, a);
+}
+
+}  // namespace
+
+extern "C" fp8_status fp8_paged_attention_workspace_size(int64_t B, int64_t Hq, int64_t H, int64_t Dh,
+                                                         int64_t max_context, int weights, int64_t tokens,
+                                                         size_t *bytes) {
+    if (!bytes) return FP8_ERR_INVALID_ARG;
+    if (max_context < 0 || max_context > kPagedMaxContext) return FP8_ERR_SHAPE;
+    fp8_status st = attn_shape(0x7FFFFFFFFFFFll, tokens, B, Hq, H, Dh, 1, 0, 0, 0, 0);
+    if (st != FP8_OK) return st;
+    if (tokens > 0) return prefill_workspace(tokens, B, Hq, H, Dh, bytes);
+    int sms;
+    st = check_device(&sms);
+    if (st != FP8_OK) return st;
+    *bytes = decode_plan(B, Hq, H, Dh, max_context, weights != 0, sms).total();
+    return FP8_OK;
+}
+
+extern "C" fp8_status fp8_paged_attention_decode(
+    const void *q_bf16, int64_t ld_q, int64_t B, int64_t Hq, const uint8_t *k_cache, const float *k_scale,
+    const uint8_t *v_cache, const float *v_scale, int64_t H, int64_t Dh, int64_t block_size, int64_t num_blocks,
+    fp8_format fmt, const int32_t *block_table, const int32_t *seq_lens, int64_t max_blocks, int64_t window,
+    int64_t sinks, float softmax_scale, void *out_bf16, float *lse, float *mass, int64_t ld_mass, float mass_decay,
+    void *workspace, size_t workspace_bytes, void *stream) {
+    if (fmt != FP8_E4M3 && fmt != FP8_E5M2) return FP8_ERR_INVALID_ARG;
+    fp8_status st = attn_shape(ld_q, B, B, Hq, H, Dh, block_size, num_blocks, max_blocks, window, sinks);
+    if (st != FP8_OK) return st;
+    if (mass && ld_mass < 0) return FP8_ERR_SHAPE;
+    if (!std::isfinite(softmax_scale) || (mass && !std::isfinite(mass_decay))) return FP8_ERR_INVALID_ARG;
+    if (B == 0) return FP8_OK;
+    st = attn_pointers(q_bf16, ld_q, k_cache, k_scale, v_cache, v_scale, num_blocks, block_table, seq_lens, max_blocks,
+                       out_bf16, workspace);
+    if (st != FP8_OK) return st;
+    int sms;
+    st = check_device(&sms);
+    if (st != FP8_OK) return st;
+    const int64_t context = max_blocks * block_size;
+    const DecodePlan p = decode_plan(B, Hq, H, Dh, context, mass != nullptr, sms);
+    if (!workspace || workspace_bytes < p.total()) return FP8_ERR_INVALID_ARG;
+    const PagedView pv = make_paged_view(k_cache, k_scale, v_cache, v_scale, H, Dh, block_size, num_blocks,
+                                         block_table, seq_lens, max_blocks, window, sinks);
+    uint8_t *ws = (uint8_t *)workspace;
+    DecodeArgs a = {};
+    a.q = (const __nv_bfloat16 *)q_bf16;
+    a.ld_q = ld_q;
+    a.B = (int)B;
+    a.G = p.G;
+    a.GC = p.GC;
+    a.HB = p.HB;
+    a.scale = softmax_scale;
+    a.out = (__nv_bfloat16 *)out_bf16;
+    a.part = (float *)ws;
+    a.lse = lse ? lse : (float *)(ws + p.part_bytes);
+    if (mass && ld_mass > 0 && context > 0) {
+        a.logits = (float *)(ws + p.part_bytes + p.lse_bytes);
+        a.vis_max = window > 0 ? std::min<int64_t>(context, (int64_t)pv.window + pv.sinks) : context;
+        if (pv.window == 0) a.vis_max = context;
+        a.mass = mass;
+        a.ld_mass = ld_mass;
+        a.decay = mass_decay;
+    }
+    cudaStream_t s = as_stream(stream);
+    cudaError_t e;
+#define FP8Q_DECODE(DH, NT) \
+    e = fmt == FP8_E4M3 ? launch_decode<FP8_E4M3, DH, NT>(pv, a, p, s) : launch_decode<FP8_E5M2, DH, NT>(pv, a, p, s)
+    if (p.DH == 64 && p.NT == 1) FP8Q_DECODE(64, 1);
+    else if (p.DH == 64) FP8Q_DECODE(64, 2);
+    else if (p.DH == 128 && p.NT == 1) FP8Q_DECODE(128, 1);
+    else if (p.DH == 128) FP8Q_DECODE(128, 2);
+    else FP8Q_DECODE(256, 1);
+#undef FP8Q_DECODE
+    return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+}

@@ -153,6 +153,8 @@ extern "C" fp8_status fp8_paged_kv_evict(uint8_t *k_cache, float *k_scale, uint8
     if (budget < 1 || budget > 0x7FFFFFFFll || sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks ||
         ld_out < 0)
         return FP8_ERR_SHAPE;
+    if (max_blocks > kPagedMaxContext / block_size || dst_max_blocks > kPagedMaxContext / block_size)
+        return FP8_ERR_SHAPE;
     const int64_t blocks = (budget * (H * Dh / 8) + 255) / 256;
     if (blocks > 0x7FFFFFFFll) return FP8_ERR_SHAPE;
     if (B == 0) return FP8_OK;

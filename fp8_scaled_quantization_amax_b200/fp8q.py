@@ -625,7 +625,7 @@ def paged_attention_decode(q, k_cache, v_cache, block_table, seq_lens, window=0,
         raise ValueError("out must have the shape of q")
     o = out if out is not None else torch.empty((B, Hq, Dh), dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    if workspace is None:
+    if workspace is None and B:
         workspace = paged_attention_workspace(B, Hq, H, Dh, mb * k_cache.block_size, mass is not None, 0, q.device)
     fp8_paged_attention_decode(q, ld_q, B, Hq, *caches, H, Dh, k_cache.block_size, k_cache.num_blocks, k_cache.fmt,
                                block_table, seq_lens, mb, window, sinks,

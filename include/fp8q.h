@@ -554,7 +554,8 @@ FP8Q_API fp8_status fp8_paged_kv_gather(const uint8_t *cache, const float *scale
  *   products with V are fp16 tensor-core products with fp32 sums; logits,
  *   maxima and sums are fp32.
  *   Shapes: Dh % 16 == 0, 16 <= Dh <= 256, H * Dh <= 8192, Hq % H == 0,
- *   B <= 65535, num_blocks * block_size < 2^31, window, sinks >= 0,
+ *   B <= 65535, num_blocks * block_size < 2^31, max_blocks * block_size <=
+ *   2^31 - 65536, window, sinks >= 0,
  *   softmax_scale and mass_decay finite.
  *   Errors: FP8_ERR_SHAPE, FP8_ERR_INVALID_ARG (NULL pointer, format, a
  *   workspace that is too small, a scale that is not finite),
@@ -596,7 +597,8 @@ FP8Q_API fp8_status fp8_paged_attention_prefill(
  * for fp8_paged_attention_decode (max_context = max_blocks * block_size and
  * weights != 0 when mass is asked for), tokens = T for
  * fp8_paged_attention_prefill (max_context and weights are then ignored).
- * The size does not grow with B beyond the weights' scratch.
+ * Apart from 4 bytes per (sequence, query head) and the weights' scratch the
+ * size does not grow with B.
  */
 FP8Q_API fp8_status fp8_paged_attention_workspace_size(int64_t B, int64_t Hq, int64_t H, int64_t Dh,
                                                        int64_t max_context, int weights, int64_t tokens,
@@ -629,7 +631,8 @@ FP8Q_API fp8_status fp8_paged_attention_workspace_size(int64_t B, int64_t Hq, in
  *               masses (those of positions below ld_out), then zeros.
  *   lens_out    [B] int32: min(n, budget); may be seq_lens itself.
  *   Shapes: Dh % 8 == 0, H * Dh <= 8192, B <= 65535, budget >= 1, sinks and
- *   recent >= 0, sinks + recent <= budget, num_blocks * block_size < 2^31.
+ *   recent >= 0, sinks + recent <= budget, num_blocks * block_size < 2^31,
+ *   max_blocks * block_size and dst_max_blocks * block_size <= 2^31 - 65536.
  *   Errors: FP8_ERR_SHAPE, FP8_ERR_INVALID_ARG (NULL pointer),
  *   FP8_ERR_ALIGNMENT (the caches: 16 bytes).
  */

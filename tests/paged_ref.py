@@ -34,6 +34,7 @@ class Cache:
     def __init__(self, k, v):
         self.fmt, self.bs, self.H, self.Dh, self.nb = k.fmt, k.block_size, k.H, k.Dh, k.num_blocks
         vals = value_table(k.fmt)
+        self.vcode, self.vscale = vals[v.cache.cpu().reshape(-1, v.H, v.Dh).long()], v.scale_inv.cpu().reshape(-1, v.H)
         self.k = vals[k.cache.cpu().reshape(-1, k.H, k.Dh).long()] * k.scale_inv.cpu().reshape(-1, k.H, 1).double()
         self.v = vals[v.cache.cpu().reshape(-1, k.H, k.Dh).long()] * v.scale_inv.cpu().reshape(-1, k.H, 1).double()
 
@@ -64,8 +65,13 @@ def attend(cache, table_row, n, p, q, h, scale, window=0, sinks=0):
     # sum |q k| bounds), one rounded scale and the factors that turn it into a power of two (4 half steps).
     ez = (Dh * 2.0 ** -23 * abs(scale) * (q.abs() @ k.abs().T) + 2.0 ** -22 * z.abs()).amax(-1)
     # The weights: exp (2 ulp and the logit's error, in numerator and sum), rounded once to fp16 (2^-11) for the
-    # product with V, at most 2^-25 of the largest weight lost to fp16's subnormals; fp32 sums; bf16 result (2^-8).
+    # product with V; fp32 sums; bf16 result (2^-8).
     tol = 2.0 ** -8 * out.abs() + (1 + 2.0 ** -8) * (2.0 ** -11 + 2.0 ** -18 + 2 * ez[:, None]) * (w @ v.abs())
+    # What fp16's subnormals lose.  The product with V takes p_j d_j f, where d_j is the row's scale, f a power of two
+    # with f max(d) >= 2^8, and p_j = exp(z_j - r) for a reference r that is at most the largest logit, so that
+    # l = sum p >= 1.  Rounding below 2^-14 is off by at most 2^-25 for each j, which reaches the result divided by f l:
+    # 2^-25 sum |code_j| / (f l) <= 2^-33 max(d) sum |code_j|.
+    tol = tol + 2.0 ** -33 * cache.vscale[ss, h].double().abs().max() * cache.vcode[ss, h].abs().sum(0)
     return dict(out=out, lse=lse, pos=js, w=w, ez=ez, tol=tol + 1e-30)
 
 

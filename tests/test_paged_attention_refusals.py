@@ -41,7 +41,7 @@ SHARED = [
     (dict(Dh=24, ld_q=512), SHAPE), (dict(Dh=272, ld_q=4096), SHAPE), (dict(Dh=0), SHAPE), (dict(Dh=8), SHAPE),
     (dict(H=0), SHAPE), (dict(H=-1), SHAPE), (dict(H=256, Hq=256, ld_q=BIG), SHAPE), (dict(Hq=7), SHAPE),
     (dict(Hq=0), SHAPE), (dict(B=-1), SHAPE), (dict(B=65536), SHAPE), (dict(bs=0), SHAPE), (dict(nb=-1), SHAPE),
-    (dict(nb=1 << 30), SHAPE), (dict(bs=1 << 31, nb=0), SHAPE), (dict(mb=-1), SHAPE), (dict(window=-1), SHAPE),
+    (dict(nb=1 << 30), SHAPE), (dict(bs=1 << 31, nb=0), SHAPE), (dict(mb=-1), SHAPE), (dict(mb=1 << 27), SHAPE), (dict(window=-1), SHAPE),
     (dict(sinks=-1), SHAPE), (dict(ld_q=504), SHAPE), (dict(ld_q=516), ALIGN),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(lens=None), INVALID), (dict(table=None), INVALID),
@@ -67,7 +67,7 @@ def test_attention_refuses_what_is_its_own():
 
 @pytest.mark.parametrize("kw,status", [
     (dict(H=0), SHAPE), (dict(Dh=12), SHAPE), (dict(H=256), SHAPE), (dict(B=-1), SHAPE), (dict(B=65536), SHAPE),
-    (dict(bs=0), SHAPE), (dict(nb=1 << 30), SHAPE), (dict(mb=-1), SHAPE), (dict(dmb=-1), SHAPE),
+    (dict(bs=0), SHAPE), (dict(nb=1 << 30), SHAPE), (dict(mb=-1), SHAPE), (dict(dmb=-1), SHAPE), (dict(mb=1 << 27), SHAPE), (dict(dmb=1 << 27), SHAPE),
     (dict(ld_mass=-1), SHAPE), (dict(ld_out=-1), SHAPE), (dict(budget=0), SHAPE), (dict(budget=1 << 31), SHAPE),
     (dict(sinks=-1), SHAPE), (dict(recent=-1), SHAPE), (dict(sinks=20, recent=13), SHAPE), (dict(sinks=BIG), SHAPE),
     (dict(recent=BIG), SHAPE), (dict(lens=None), INVALID), (dict(kept=None), INVALID), (dict(mo=None), INVALID),
