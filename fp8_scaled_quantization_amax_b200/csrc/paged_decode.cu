@@ -6,8 +6,8 @@
 // once per group of query heads, so the kernel is bound by reading the cache:
 // what it has to reach is the HBM rate, and what stands against that is the
 // instructions spent on each byte.  Hence:
-//   * a warp owns one KV head and 16 positions at a time, copied by cp.async
-//     (16 bytes a lane, a few tiles ahead) into shared memory slots that the
+//   * a warp owns one KV head and 32 positions at a time, copied by cp.async
+//     (16 bytes a lane, K and V in turn, two halves ahead) into shared memory slots that the
 //     same lane reads back, so no barrier stands between copy and use;
 //   * the copied bytes are matrix fragments as they lie: any permutation of
 //     the head elements is allowed in K Q^T when Q is permuted alike (lane t of
@@ -41,7 +41,7 @@ using namespace fp8q;
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kTile = 16;                    // positions per warp and step
+constexpr int kTile = 32;                    // positions per warp and step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.0e38f;           // before the first logit; below every finite logit that matters
 constexpr float kLazy = 6.0f;                // log2 of how far a logit may pass the maximum in use
@@ -61,14 +61,19 @@ struct DecodeArgs {
     float decay;
 };
 
+// A warp's ring of UNITS tile halves: K of 32 positions, then V of the same,
+// each with its 32 scales (and, K, the mask of live positions).  Three halves
+// keep two (8 KiB at a head size of 128) in flight per warp, which at 16 warps
+// is 134 KiB per SM, more than the HBM rate needs at its latency.
 template <int DH, int NT>
 struct Cfg {
-    static constexpr int STAGE = 32 * DH + 128 + 16;     // K, V, 32 scales, the mask of live positions
+    static constexpr int UNIT = 32 * DH + 128 + 16;
     static constexpr int MIN_CTAS = (DH <= 128 && NT == 1) ? 2 : 1;
-    static constexpr int STAGES = DH == 64 ? 5 : DH == 128 ? (NT == 1 ? 3 : 5) : 3;
-    static constexpr size_t SMEM = (size_t)kWarps * STAGES * STAGE;
+    static constexpr int UNITS = DH == 64 ? 6 : DH == 128 ? (NT == 1 ? 3 : 6) : 3;
+    static constexpr int WARP_BYTES = UNITS * UNIT;
+    static constexpr size_t SMEM = (size_t)kWarps * WARP_BYTES;
     static constexpr int COLS = 8 * NT;                  // query heads per chunk
-    static_assert(STAGES * STAGE >= COLS * DH * 4, "the warps' results are merged in the pipeline's memory");
+    static_assert(WARP_BYTES >= COLS * DH * 4, "the warps' results are merged in the pipeline's memory");
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -239,8 +244,8 @@ k_decode(const PagedView pv, const DecodeArgs a) {
     int nt = (vis.count + per_tile - 1) / per_tile;
     int row = (int)((at - s_before) / nt), tile = (int)((at - s_before) % nt);
 
-    const uint32_t sm = smem_addr(smem) + (uint32_t)(warp * C::STAGES * C::STAGE);
-    const int64_t row_bytes = (int64_t)pv.H * pv.Dh;
+    const uint32_t sm = smem_addr(smem) + (uint32_t)(warp * C::WARP_BYTES);
+    const uint32_t row_bytes = (uint32_t)(pv.H * pv.Dh);
 
     while (true) {
         const int tile_end = (int)min((int64_t)nt, tile + (end - at));
@@ -296,116 +301,144 @@ k_decode(const PagedView pv, const DecodeArgs a) {
             l[x][0] = l[x][1] = 0.0f;
         }
 
-        const uint8_t *kh = pv.kc + (int64_t)h * pv.Dh, *vhp = pv.vc + (int64_t)h * pv.Dh;
+        const uint8_t *kh = pv.kc + (int64_t)h * pv.Dh + 16 * t, *vhp = pv.vc + (int64_t)h * pv.Dh + VB * g;
+        const float *ksh = pv.ks + h, *vsh = pv.vs + h;
         const int ntile = tile_end - tile;
-        // slot of this lane's position (lanes 16.. repeat 0..15) of the k-th tile
-        auto slot_of = [&](int k) {
-            const int i = ((tile + k) * WT + wt) * kTile + (lane & 15);
-            return k < ntile && i < vis.count ? pv.slot(b, vis.position(i)) : -1;
-        };
-        int next_slot = slot_of(0);
-        auto issue = [&](int k) {             // copies of the k-th tile
-            if (k < ntile) {
-                const uint32_t st = sm + (uint32_t)(k % C::STAGES) * C::STAGE;
-                const int slot = next_slot;
+        // index of this lane's position in the tile whose copies come next, and its slot
+        int fetch = (tile * WT + wt) * kTile + lane;
+        const int fetch_end = tile_end * WT * kTile + lane;        // tiles from there on are not this run's
+        auto slot_at = [&](int i) { return i < vis.count ? pv.slot(b, vis.position(i)) : -1; };
+        int slot = slot_at(fetch);
+        uint32_t fill = sm, read = sm;        // units of the ring to copy into and to read
+        auto issue_k = [&] {                  // K of the next tile
+            if (fetch < fetch_end) {          // the same for all lanes
                 const uint32_t live = __ballot_sync(0xFFFFFFFFu, slot >= 0);
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
+                for (int r = 0; r < 4; ++r) {
                     const int s = __shfl_sync(0xFFFFFFFFu, slot, g + 8 * r);
-                    const uint8_t *src = kh + (int64_t)max(s, 0) * row_bytes + 16 * t;
+                    const uint8_t *src = kh + (uint64_t)(uint32_t)max(s, 0) * row_bytes;
 #pragma unroll
                     for (int c = 0; c < KC; ++c)
-                        cp_async<16>(st + (uint32_t)(((r * KC + c) * 32 + lane) * 16), src + 64 * c,
+                        cp_async<16>(fill + (uint32_t)(((r * KC + c) * 32 + lane) * 16), src + 64 * c,
                                      s >= 0 && 16 * (t + 4 * c) < pv.Dh);
                 }
-                const uint32_t sv = st + 16 * DH;
+                cp_async<4>(fill + 32 * DH + 4 * lane, ksh + (uint64_t)(uint32_t)max(slot, 0) * (uint32_t)pv.H, slot >= 0);
+                if (lane == 0)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(fill + 32 * DH + 128), "r"(live) : "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            fill = fill + C::UNIT == sm + C::WARP_BYTES ? sm : fill + C::UNIT;
+        };
+        auto issue_v = [&] {                  // V of the same tile; then the next tile's slots
+            if (fetch < fetch_end) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int s = __shfl_sync(0xFFFFFFFFu, slot, 2 * t + (e & 1) + 4 * (e & 2));
-                    const uint8_t *src = vhp + (int64_t)max(s, 0) * row_bytes + VB * g;
+                for (int e = 0; e < 8; ++e) {
+                    const int s = __shfl_sync(0xFFFFFFFFu, slot, 2 * t + (e & 1) + 4 * (e & 2) + 4 * (e & 4));
+                    const uint8_t *src = vhp + (uint64_t)(uint32_t)max(s, 0) * row_bytes;
                     if constexpr (VB == 8) {
-                        cp_async<8>(sv + (uint32_t)((e * 32 + lane) * 8), src, s >= 0 && 8 * g < pv.Dh);
+                        cp_async<8>(fill + (uint32_t)((e * 32 + lane) * 8), src, s >= 0 && 8 * g < pv.Dh);
                     } else {
 #pragma unroll
                         for (int c = 0; c < VB / 16; ++c)
-                            cp_async<16>(sv + (uint32_t)(((e * (VB / 16) + c) * 32 + lane) * 16), src + 16 * c,
+                            cp_async<16>(fill + (uint32_t)(((e * (VB / 16) + c) * 32 + lane) * 16), src + 16 * c,
                                          s >= 0 && VB * g + 16 * c < pv.Dh);
                     }
                 }
-                const float *sp = (lane < 16 ? pv.ks : pv.vs) + (int64_t)max(slot, 0) * pv.H + h;
-                cp_async<4>(st + 32 * DH + 4 * lane, sp, slot >= 0);
-                if (lane == 0)
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + 32 * DH + 128), "r"(live) : "memory");
-                next_slot = slot_of(k + 1);
+                cp_async<4>(fill + 32 * DH + 4 * lane, vsh + (uint64_t)(uint32_t)max(slot, 0) * (uint32_t)pv.H, slot >= 0);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
+            fill = fill + C::UNIT == sm + C::WARP_BYTES ? sm : fill + C::UNIT;
+            fetch += WT * kTile;
+            slot = slot_at(fetch);
         };
-        for (int k = 0; k < C::STAGES - 1; ++k) issue(k);
+        // the ring's last unit is filled when the one that was read before it is done with
+#pragma unroll
+        for (int u = 0; u < C::UNITS - 1; ++u) {
+            if (u % 2 == 0) issue_k(); else issue_v();
+        }
 
         for (int k = 0; k < ntile; ++k) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(C::STAGES - 2) : "memory");
-            __syncwarp();                     // the other lanes' scales; and tile k - 1 is read by all
-            issue(k + C::STAGES - 1);
-            const uint32_t st = sm + (uint32_t)(k % C::STAGES) * C::STAGE, sc = st + 32 * DH;
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::UNITS - 2) : "memory");
+            __syncwarp();                     // the other lanes' scales; and the unit read before is done with
+            if constexpr (C::UNITS % 2) issue_k(); else issue_v();
             uint32_t live;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(live) : "r"(sc + 128));
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(live) : "r"(read + 32 * DH + 128));
 
-            // ---- S^T = K Q^T
-            float s[NT][4];
+            // ---- S^T = K Q^T, 16 positions at a time
+            float s[2][NT][4];
 #pragma unroll
-            for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.0f;
+            for (int y = 0; y < 2; ++y) {
 #pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                const uint4 k0 = lds128(st + (uint32_t)((c * 32 + lane) * 16));
-                const uint4 k1 = lds128(st + (uint32_t)(((KC + c) * 32 + lane) * 16));
-                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+                for (int x = 0; x < NT; ++x) s[y][x][0] = s[y][x][1] = s[y][x][2] = s[y][x][3] = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t a0 = to_f16x2<FMT>(w0[i]), a2 = to_f16x2<FMT>(w0[i] >> 16);
-                    const uint32_t a1 = to_f16x2<FMT>(w1[i]), a3 = to_f16x2<FMT>(w1[i] >> 16);
+                for (int c = 0; c < KC; ++c) {
+                    const uint4 k0 = lds128(read + (uint32_t)(((2 * y * KC + c) * 32 + lane) * 16));
+                    const uint4 k1 = lds128(read + (uint32_t)((((2 * y + 1) * KC + c) * 32 + lane) * 16));
+                    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-                    for (int x = 0; x < NT; ++x) mma16816(s[x], a0, a1, a2, a3, qf[x][c * 4 + i][0], qf[x][c * 4 + i][1]);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a0 = to_f16x2<FMT>(w0[i]), a2 = to_f16x2<FMT>(w0[i] >> 16);
+                        const uint32_t a1 = to_f16x2<FMT>(w1[i]), a3 = to_f16x2<FMT>(w1[i] >> 16);
+#pragma unroll
+                        for (int x = 0; x < NT; ++x)
+                            mma16816(s[y][x], a0, a1, a2, a3, qf[x][c * 4 + i][0], qf[x][c * 4 + i][1]);
+                    }
                 }
             }
             // ---- logits in log2 units; what is not visible becomes -inf
-            const float dk0 = lds_f(sc + 4 * g), dk1 = lds_f(sc + 4 * (g + 8));
-            const float dv0 = lds_f(sc + 4 * (g + 16)), dv1 = lds_f(sc + 4 * (g + 24));
             bool up = false;
 #pragma unroll
-            for (int x = 0; x < NT; ++x) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    s[x][e] *= dk0 * cf[x][e];
-                    s[x][2 + e] *= dk1 * cf[x][e];
-                }
-                if (live != 0xFFFFFFFFu) {
-                    if (!((live >> g) & 1u)) s[x][0] = s[x][1] = -INFINITY;
-                    if (!((live >> (g + 8)) & 1u)) s[x][2] = s[x][3] = -INFINITY;
-                }
-                up |= fmaxf(s[x][0], s[x][2]) > m[x][0] + kLazy || fmaxf(s[x][1], s[x][3]) > m[x][1] + kLazy;
-            }
-            if (a.logits) {
-                const int i0 = ((tile + k) * WT + wt) * kTile;
-                float *lp = a.logits + (((int64_t)b * VH + vh) * a.vis_max + i0) * C::COLS + 2 * t;
+            for (int y = 0; y < 2; ++y) {
+                const float dk0 = lds_f(read + 32 * DH + 4 * (16 * y + g));
+                const float dk1 = lds_f(read + 32 * DH + 4 * (16 * y + g + 8));
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
-                    if (i0 + g < vis.count)
-                        *reinterpret_cast<float2 *>(lp + g * C::COLS + 8 * x) = make_float2(s[x][0], s[x][1]);
-                    if (i0 + g + 8 < vis.count)
-                        *reinterpret_cast<float2 *>(lp + (g + 8) * C::COLS + 8 * x) = make_float2(s[x][2], s[x][3]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        s[y][x][e] *= dk0 * cf[x][e];
+                        s[y][x][2 + e] *= dk1 * cf[x][e];
+                    }
                 }
             }
+            if (live != 0xFFFFFFFFu) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int x = 0; x < NT; ++x) {
+                        if (!((live >> (16 * y + g)) & 1u)) s[y][x][0] = s[y][x][1] = -INFINITY;
+                        if (!((live >> (16 * y + g + 8)) & 1u)) s[y][x][2] = s[y][x][3] = -INFINITY;
+                    }
+            }
+            if (a.logits) {
+                const int i0 = ((tile + k) * WT + wt) * kTile + g;
+                float *lp = a.logits + (((int64_t)b * VH + vh) * a.vis_max + i0) * C::COLS + 2 * t;
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+                        if (i0 + 8 * y < vis.count)
+                            *reinterpret_cast<float2 *>(lp + 8 * y * C::COLS + 8 * x) =
+                                make_float2(s[y / 2][x][2 * (y & 1)], s[y / 2][x][2 * (y & 1) + 1]);
+            }
+            float mx[NT][2];
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[x][e] = fmaxf(fmaxf(s[0][x][e], s[0][x][2 + e]), fmaxf(s[1][x][e], s[1][x][2 + e]));
+                    up |= mx[x][e] > m[x][e] + kLazy;
+                }
             if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
                 for (int x = 0; x < NT; ++x)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(m[x][e], fmaxf(s[x][e], s[x][2 + e]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-                        const float al = exp2_fast(m[x][e] - mx);
-                        m[x][e] = mx;
+                        float v = fmaxf(m[x][e], mx[x][e]);
+                        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+                        const float al = exp2_fast(m[x][e] - v);
+                        m[x][e] = v;
                         l[x][e] *= al;
 #pragma unroll
                         for (int i = 0; i < MI; ++i) {
@@ -414,11 +447,28 @@ k_decode(const PagedView pv, const DecodeArgs a) {
                         }
                     }
             }
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[y][x][e] = exp2_fast(s[y][x][e] - m[x][e & 1]);
+                        l[x][e & 1] += s[y][x][e];
+                    }
+            read = read + C::UNIT == sm + C::WARP_BYTES ? sm : read + C::UNIT;
+
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::UNITS - 2) : "memory");
+            __syncwarp();
+            if constexpr (C::UNITS % 2) issue_v(); else issue_k();
             // ---- the power of two that V's scales are held against
-            const float dmax = fmaxf(fabsf(dv0), fabsf(dv1));
+            float dv[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) dv[y] = lds_f(read + 32 * DH + 4 * (8 * y + g));
+            const float dmax = fmaxf(fmaxf(fabsf(dv[0]), fabsf(dv[1])), fmaxf(fabsf(dv[2]), fabsf(dv[3])));
             if (__any_sync(0xFFFFFFFFu, dmax > vcap && dmax < INFINITY)) {
                 const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, dmax < INFINITY ? __float_as_uint(dmax) : 0u);
-                const int ex = max((int)(bits >> 23) - 127, -100);   // dmax < 2^(ex + 1)
+                const int ex = max((int)(bits >> 23) - 127, -100);             // dmax < 2^(ex + 1)
                 const float vs = pow2i(8 - ex), r = vcap > 0.0f ? vs / vscale : 1.0f;
                 vscale = vs;                                                   // dv * vscale < 2^9
                 vcap = pow2i(ex + 1);
@@ -429,45 +479,47 @@ k_decode(const PagedView pv, const DecodeArgs a) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[x][i][e] *= r;
             }
-            const float f0 = dv0 * vscale, f1 = dv1 * vscale;
-            uint32_t pb[NT][2];
+            uint32_t pb[2][NT][2];
 #pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                const float p0 = exp2_fast(s[x][0] - m[x][0]), p1 = exp2_fast(s[x][1] - m[x][1]);
-                const float p2 = exp2_fast(s[x][2] - m[x][0]), p3 = exp2_fast(s[x][3] - m[x][1]);
-                l[x][0] += p0 + p2;
-                l[x][1] += p1 + p3;
-                pb[x][0] = transpose8x8(pack_f16x2(p0 * f0, p1 * f0));
-                pb[x][1] = transpose8x8(pack_f16x2(p2 * f1, p3 * f1));
+            for (int y = 0; y < 2; ++y) {
+                const float f0 = dv[2 * y] * vscale, f1 = dv[2 * y + 1] * vscale;
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+                    pb[y][x][0] = transpose8x8(pack_f16x2(s[y][x][0] * f0, s[y][x][1] * f0));
+                    pb[y][x][1] = transpose8x8(pack_f16x2(s[y][x][2] * f1, s[y][x][3] * f1));
+                }
             }
             // ---- O^T += V^T P^T
-            const uint32_t sv = st + 16 * DH;
 #pragma unroll
-            for (int c = 0; c < (VB + 15) / 16; ++c) {
-                uint32_t v[4][4];
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (VB == 8) {
-                        const uint2 w = lds64(sv + (uint32_t)((e * 32 + lane) * 8));
-                        v[e][0] = w.x; v[e][1] = w.y;
-                    } else {
-                        const uint4 w = lds128(sv + (uint32_t)(((e * (VB / 16) + c) * 32 + lane) * 16));
-                        v[e][0] = w.x; v[e][1] = w.y; v[e][2] = w.z; v[e][3] = w.w;
+                for (int c = 0; c < (VB + 15) / 16; ++c) {
+                    uint32_t v[4][4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (VB == 8) {
+                            const uint2 w = lds64(read + (uint32_t)(((4 * y + e) * 32 + lane) * 8));
+                            v[e][0] = w.x; v[e][1] = w.y;
+                        } else {
+                            const uint4 w = lds128(read + (uint32_t)((((4 * y + e) * (VB / 16) + c) * 32 + lane) * 16));
+                            v[e][0] = w.x; v[e][1] = w.y; v[e][2] = w.z; v[e][3] = w.w;
+                        }
                     }
+#pragma unroll
+                    for (int w = 0; w < (VB == 8 ? 2 : 4); ++w)
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const uint32_t sel = hf ? 0x7362u : 0x5140u;
+                            const uint32_t xx = __byte_perm(v[0][w], v[1][w], sel);
+                            const uint32_t yy = __byte_perm(v[2][w], v[3][w], sel);
+                            const uint32_t a0 = to_f16x2<FMT>(xx), a1 = to_f16x2<FMT>(xx >> 16);
+                            const uint32_t a2 = to_f16x2<FMT>(yy), a3 = to_f16x2<FMT>(yy >> 16);
+#pragma unroll
+                            for (int x = 0; x < NT; ++x)
+                                mma16816(o[x][c * 8 + w * 2 + hf], a0, a1, a2, a3, pb[y][x][0], pb[y][x][1]);
+                        }
                 }
-#pragma unroll
-                for (int w = 0; w < (VB == 8 ? 2 : 4); ++w)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const uint32_t sel = hf ? 0x7362u : 0x5140u;
-                        const uint32_t xx = __byte_perm(v[0][w], v[1][w], sel), yy = __byte_perm(v[2][w], v[3][w], sel);
-                        const uint32_t a0 = to_f16x2<FMT>(xx), a1 = to_f16x2<FMT>(xx >> 16);
-                        const uint32_t a2 = to_f16x2<FMT>(yy), a3 = to_f16x2<FMT>(yy >> 16);
-#pragma unroll
-                        for (int x = 0; x < NT; ++x)
-                            mma16816(o[x][c * 8 + w * 2 + hf], a0, a1, a2, a3, pb[x][0], pb[x][1]);
-                    }
-            }
+            read = read + C::UNIT == sm + C::WARP_BYTES ? sm : read + C::UNIT;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
 
@@ -522,7 +574,7 @@ k_decode(const PagedView pv, const DecodeArgs a) {
                 }
         } else {
             __syncthreads();                  // every warp's copies have landed and been read
-            float *mine = reinterpret_cast<float *>(smem + (size_t)warp * C::STAGES * C::STAGE);
+            float *mine = reinterpret_cast<float *>(smem + (size_t)warp * C::WARP_BYTES);
 #pragma unroll
             for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -550,7 +602,7 @@ k_decode(const PagedView pv, const DecodeArgs a) {
                 for (int w = 0; w < WT; ++w) {
                     const float al = exp2_fast(s_m[hh * WT + w][col] - mx);
                     const float4 v = *reinterpret_cast<const float4 *>(
-                        smem + (size_t)(hh * WT + w) * C::STAGES * C::STAGE + (size_t)(col * DH + d) * 4);
+                        smem + (size_t)(hh * WT + w) * C::WARP_BYTES + (size_t)(col * DH + d) * 4);
                     sum = fmaf(s_l[hh * WT + w][col], al, sum);
                     acc.x = fmaf(v.x, al, acc.x); acc.y = fmaf(v.y, al, acc.y);
                     acc.z = fmaf(v.z, al, acc.z); acc.w = fmaf(v.w, al, acc.w);
@@ -587,12 +639,13 @@ k_decode(const PagedView pv, const DecodeArgs a) {
 // Joins the parts of the rows that more than one CTA worked on, and writes the
 // results of queries that see nothing.  One CTA per (sequence, query head):
 // a warp per part, a lane per DH / 32 elements.
+constexpr int kJoinWarps = 8;
 template <int DH, int COLS>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoinWarps * 32)
 k_decode_join(const PagedView pv, const DecodeArgs a, int64_t grid) {
     constexpr int E = DH / 32;
-    __shared__ int64_t scan_buf[4];
-    __shared__ float s_acc[4][DH], s_ml[4][2];
+    __shared__ int64_t scan_buf[kJoinWarps];
+    __shared__ float s_acc[kJoinWarps][DH], s_sum[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int Hq = pv.H * a.G, b = (int)(blockIdx.x / Hq), hq = (int)(blockIdx.x % Hq), h = hq / a.G, gi = hq % a.G;
     const int WT = kWarps / a.HB, VH = pv.H * a.GC, rows = VH / a.HB, per_tile = kTile * WT;
@@ -601,7 +654,7 @@ k_decode_join(const PagedView pv, const DecodeArgs a, int64_t grid) {
     pdl_wait();
     const int nt = tiles_of(pv, b, per_tile);
     if (nt == 0) {
-        for (int d = threadIdx.x; d < pv.Dh; d += 128) a.out[orow * pv.Dh + d] = __float2bfloat16(0.0f);
+        for (int d = threadIdx.x; d < pv.Dh; d += kJoinWarps * 32) a.out[orow * pv.Dh + d] = __float2bfloat16(0.0f);
         if (threadIdx.x == 0) a.lse[orow] = -INFINITY;
         return;
     }
@@ -616,39 +669,36 @@ k_decode_join(const PagedView pv, const DecodeArgs a, int64_t grid) {
     const int64_t stride = (int64_t)a.HB * COLS * (DH + 2), ml = (int64_t)a.HB * COLS * DH + 2 * pc;
     // the row's tile 0 is in c0, whose part is the second of its two; the others' is their first
     auto part = [&](int64_t c) { return a.part + (2 * c + (c == c0 ? 1 : 0)) * stride; };
-    float mx = kNoMax, sum = 0.0f, acc[E];
+    // the largest maximum first (a lane per part), then independent loads of the sums
+    float mx = kNoMax;
+    for (int64_t c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, part(c)[ml]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    float sum = 0.0f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int64_t c = c0 + warp; c <= c1; c += 4) {
+#pragma unroll 4
+    for (int64_t c = c0 + warp; c <= c1; c += kJoinWarps) {
         const float *p = part(c);
         const float2 v = *reinterpret_cast<const float2 *>(p + ml);
-        const float nm = fmaxf(mx, v.x), al = exp2_fast(mx - nm), be = exp2_fast(v.x - nm);
-        mx = nm;
-        sum = sum * al + v.y * be;
+        const float be = exp2_fast(v.x - mx);
+        sum = fmaf(v.y, be, sum);
         const float *o = p + (int64_t)pc * DH + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * al + o[e] * be;
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(o[e], be, acc[e]);
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-    if (lane == 0) {
-        s_ml[warp][0] = mx;
-        s_ml[warp][1] = sum;
-    }
+    if (lane == 0) s_sum[warp] = sum;
     __syncthreads();
-    mx = fmaxf(fmaxf(s_ml[0][0], s_ml[1][0]), fmaxf(s_ml[2][0], s_ml[3][0]));
-    float al[4];
     sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        al[w] = exp2_fast(s_ml[w][0] - mx);
-        sum = fmaf(s_ml[w][1], al[w], sum);
-    }
+    for (int w = 0; w < kJoinWarps; ++w) sum += s_sum[w];
     const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
-    for (int d = threadIdx.x; d < pv.Dh; d += 128) {
+    for (int d = threadIdx.x; d < pv.Dh; d += kJoinWarps * 32) {
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) v = fmaf(s_acc[w][d], al[w], v);
+        for (int w = 0; w < kJoinWarps; ++w) v += s_acc[w][d];
         a.out[orow * pv.Dh + d] = __float2bfloat16(v * r);
     }
     if (threadIdx.x == 0) a.lse[orow] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
@@ -731,7 +781,7 @@ cudaError_t launch_decode(const PagedView &pv, const DecodeArgs &a, const Decode
     if (e != cudaSuccess) return e;
     e = pdl_launch(k_decode<FMT, DH, NT>, dim3(p.ctas), dim3(kWarps * 32), C::SMEM, s, pv, a);
     if (e != cudaSuccess) return e;
-    e = pdl_launch(k_decode_join<DH, C::COLS>, dim3((unsigned)(a.B * (int64_t)pv.H * a.G)), dim3(128), 0, s, pv, a,
+    e = pdl_launch(k_decode_join<DH, C::COLS>, dim3((unsigned)(a.B * (int64_t)pv.H * a.G)), dim3(kJoinWarps * 32), 0, s, pv, a,
                    (int64_t)p.ctas);
     if (e != cudaSuccess || !a.logits) return e;
     // eight CTAs per SM in all, or one per (sequence, head) where there are more of those
