@@ -1041,6 +1041,7 @@ extern "C" fp8_status fp8_gemm_block_requant(const uint8_t *A, fp8_format fa, co
 fp8_status fp8q_mx_device_error(uint32_t *out, int clear);
 fp8_status fp8q_wgrad_device_error(uint32_t *out, int clear);
 fp8_status fp8q_block_device_error(uint32_t *out, int clear);
+fp8_status fp8q_decode_device_error(uint32_t *out, int clear);
 
 extern "C" fp8_status fp8_device_error(uint32_t *host_out, int clear) {
     if (!host_out) return FP8_ERR_INVALID_ARG;
@@ -1055,7 +1056,10 @@ extern "C" fp8_status fp8_device_error(uint32_t *host_out, int clear) {
     uint32_t b = 0;
     st = fp8q_block_device_error(&b, clear);
     if (st != FP8_OK) return st;
-    *host_out = v | w | g | b;
+    uint32_t d = 0;
+    st = fp8q_decode_device_error(&d, clear);
+    if (st != FP8_OK) return st;
+    *host_out = v | w | g | b | d;
     if (clear) {
         const unsigned int z = 0;
         if (cudaMemcpyToSymbol(g_gemm_error, &z, sizeof(z)) != cudaSuccess) return FP8_ERR_CUDA;

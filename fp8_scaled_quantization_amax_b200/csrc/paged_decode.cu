@@ -6,9 +6,10 @@
 // once per group of query heads, so the kernel is bound by reading the cache:
 // what it has to reach is the HBM rate, and what stands against that is the
 // instructions spent on each byte.  Hence:
-//   * a warp owns one KV head and 32 positions at a time, copied by cp.async
-//     (16 bytes a lane, K and V in turn, two halves ahead) into shared memory slots that the
-//     same lane reads back, so no barrier stands between copy and use;
+//   * a warp owns one KV head and 32 positions at a time.  Its K and V tiles
+//     come by TMA into a ring in shared memory (boxes of 8, 16 or 32 rows of one
+//     head, whatever divides the page size; pages of another size take
+//     cp.async into the same layout), with no other warp to wait for;
 //   * the copied bytes are matrix fragments as they lie: any permutation of
 //     the head elements is allowed in K Q^T when Q is permuted alike (lane t of
 //     a row takes whole 16-byte chunks), and any permutation of V's columns
@@ -35,6 +36,7 @@
 #include <atomic>
 
 #include "paged_attn.cuh"
+#include "tc.cuh"
 
 using namespace fp8q;
 
@@ -49,6 +51,7 @@ constexpr float kLazy = 6.0f;                // log2 of how far a logit may pass
 struct DecodeArgs {
     const __nv_bfloat16 *q;
     int64_t ld_q;
+    int box;                 // rows per TMA box: 8, 16 or 32
     int B, G, GC, HB;        // query heads per KV head; chunks of them; (virtual) heads per CTA
     float scale;
     __nv_bfloat16 *out;
@@ -67,16 +70,15 @@ struct DecodeArgs {
 // is 134 KiB per SM, more than the HBM rate needs at its latency.
 template <int DH, int NT>
 struct Cfg {
-    static constexpr int UNIT = 32 * DH + 128 + 16;
+    static constexpr int UNIT = 32 * DH, AUX = 128 + 16;
     static constexpr int MIN_CTAS = (DH <= 128 && NT == 1) ? 2 : 1;
     static constexpr int UNITS = DH == 64 ? 6 : DH == 128 ? (NT == 1 ? 3 : 6) : 3;
-    static constexpr int WARP_BYTES = UNITS * UNIT;
-    static constexpr size_t SMEM = (size_t)kWarps * WARP_BYTES;
+    static constexpr int AUX_OFF = kWarps * UNITS * UNIT, BAR_OFF = AUX_OFF + kWarps * UNITS * AUX;
+    static constexpr size_t SMEM = 1024 + BAR_OFF + kWarps * UNITS * 8;
     static constexpr int COLS = 8 * NT;                  // query heads per chunk
-    static_assert(WARP_BYTES >= COLS * DH * 4, "the warps' results are merged in the pipeline's memory");
+    static_assert(UNITS * UNIT >= COLS * DH * 4, "the warps' results are merged in the pipeline's memory");
 };
 
-__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 // copies BYTES, or writes zeros when !live
 template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool live) {
@@ -84,8 +86,14 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool liv
     if constexpr (BYTES == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n)
-                     : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
@@ -134,25 +142,31 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // 2^e for -126 <= e <= 127; infinity at 128
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// Visible positions of the one query of sequence b: index i < sinks is
-// position i, the others follow from `begin`.
+// Visible positions of the one query of sequence b: [0, sinks) and [begin, n).
+// Its tiles hold 32 aligned positions each: those of the sinks, then those of
+// the window, without the ones that are already there.
 struct Visible {
-    int begin, sinks, count;
-    __device__ __forceinline__ int position(int i) const { return i < sinks ? i : begin + (i - sinks); }
+    int begin, sinks, n, sink_tiles, first_tile, tiles;
+    __device__ __forceinline__ int position(int tile) const {   // first of a tile
+        return (tile < sink_tiles ? tile : first_tile + (tile - sink_tiles)) * kTile;
+    }
+    __device__ __forceinline__ bool sees(int j) const { return j < n && (j >= begin || j < sinks); }
 };
 __device__ __forceinline__ Visible visible_of(const PagedView &pv, int64_t b) {
-    const int n = pv.length(b);
     Visible v;
-    v.begin = pv.window_begin(n - 1);
+    v.n = pv.length(b);
+    v.begin = pv.window_begin(v.n - 1);
     v.sinks = min(pv.sinks, v.begin);
-    v.count = n - v.begin + v.sinks;
+    v.first_tile = v.begin / kTile;
+    v.sink_tiles = min((int)(((uint32_t)v.sinks + kTile - 1) / kTile), v.first_tile);
+    v.tiles = v.sink_tiles + (int)(((uint32_t)v.n + kTile - 1) / kTile) - v.first_tile;
     return v;
 }
 
-// Tiles laid end to end: rows (b, hb) with b slowest; nt_b tiles in each row of
-// sequence b.
-__device__ __forceinline__ int tiles_of(const PagedView &pv, int64_t b, int per_tile) {
-    return (visible_of(pv, b).count + per_tile - 1) / per_tile;
+// Tiles of WT * 32 positions laid end to end: rows (b, hb) with b slowest, as
+// many tiles in each row of a sequence as its visible positions fill.
+__device__ __forceinline__ int tiles_of(const PagedView &pv, int64_t b, int WT) {
+    return (visible_of(pv, b).tiles + WT - 1) / WT;
 }
 __device__ int64_t block_scan(int64_t v, int64_t *buf, int64_t *total) {   // exclusive
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -174,11 +188,11 @@ __device__ int64_t block_scan(int64_t v, int64_t *buf, int64_t *total) {   // ex
     return base + x - v;
 }
 // Block-wide: the tiles of all sequences, and those of the sequences before `b`.
-__device__ void count_tiles(const PagedView &pv, int B, int per_tile, int rows, int b, int64_t *buf, int64_t *total,
+__device__ void count_tiles(const PagedView &pv, int B, int WT, int rows, int b, int64_t *buf, int64_t *total,
                             int64_t *before) {
     int64_t all = 0, pre = 0;
     for (int i = threadIdx.x; i < B; i += blockDim.x) {
-        const int64_t n = (int64_t)tiles_of(pv, i, per_tile) * rows;
+        const int64_t n = (int64_t)tiles_of(pv, i, WT) * rows;
         all += n;
         if (i < b) pre += n;
     }
@@ -188,15 +202,19 @@ __device__ void count_tiles(const PagedView &pv, int B, int per_tile, int rows, 
 // First tile of CTA c of n when `total` tiles are dealt out evenly.
 __device__ __forceinline__ int64_t deal(int64_t total, int64_t n, int64_t c) { return total * c / n; }
 
-template <int FMT, int DH, int NT>
+// TMA: boxes of a.box rows, which divides the page size; otherwise cp.async.
+template <int FMT, int DH, int NT, bool TMA>
 __global__ void __launch_bounds__(kWarps * 32, Cfg<DH, NT>::MIN_CTAS)
-k_decode(const PagedView pv, const DecodeArgs a) {
+k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedView pv,
+         const DecodeArgs a) {
     using C = Cfg<DH, NT>;
     constexpr int KC = DH / 64;              // 16-byte chunks of a K row per lane
     constexpr int VB = DH / 8;               // V bytes of a position per lane
     constexpr int KS = DH / 16;              // k steps of K Q^T
     constexpr int MI = DH / 16;              // row blocks of O^T
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint32_t s_abort;
     __shared__ int64_t scan_buf[kWarps], s_before;
     __shared__ int s_b;
     __shared__ float s_m[kWarps][C::COLS], s_l[kWarps][C::COLS];
@@ -204,7 +222,19 @@ k_decode(const PagedView pv, const DecodeArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int WT = kWarps / a.HB;            // warps that share a head, a tile of positions each
     const int hw = warp / WT, wt = warp % WT;
-    const int VH = pv.H * a.GC, rows = VH / a.HB, per_tile = kTile * WT;
+    const int VH = pv.H * a.GC, rows = VH / a.HB;
+    const uint32_t data = smem_u32(smem) + (uint32_t)(warp * C::UNITS * C::UNIT);
+    const uint32_t aux = smem_u32(smem) + (uint32_t)(C::AUX_OFF + warp * C::UNITS * C::AUX);
+    const uint32_t bars = smem_u32(smem) + (uint32_t)(C::BAR_OFF + warp * C::UNITS * 8);
+    if (TMA && lane == 0) {
+        for (int u = 0; u < C::UNITS; ++u) mbar_init(bars + 8 * u, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (warp == 0) {
+            s_abort = 0u;
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK)) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmV)) : "memory");
+        }
+    }
     pdl_wait();
     pdl_trigger();
 
@@ -212,9 +242,9 @@ k_decode(const PagedView pv, const DecodeArgs a) {
     int64_t total, unused;
     int64_t mine = 0;
     if (a.B <= kWarps * 32) {
-        if (threadIdx.x < a.B) mine = (int64_t)tiles_of(pv, threadIdx.x, per_tile) * rows;
+        if (threadIdx.x < a.B) mine = (int64_t)tiles_of(pv, threadIdx.x, WT) * rows;
     } else {
-        count_tiles(pv, a.B, per_tile, rows, 0, scan_buf, &total, &unused);
+        count_tiles(pv, a.B, WT, rows, 0, scan_buf, &total, &unused);
     }
     int64_t pre = 0;
     if (a.B <= kWarps * 32) pre = block_scan(mine, scan_buf, &total);
@@ -225,7 +255,7 @@ k_decode(const PagedView pv, const DecodeArgs a) {
     for (int64_t b0 = 0, base = 0;; b0 += kWarps * 32) {
         if (a.B > kWarps * 32) {
             const int64_t bb = b0 + threadIdx.x;
-            mine = bb < a.B ? (int64_t)tiles_of(pv, bb, per_tile) * rows : 0;
+            mine = bb < a.B ? (int64_t)tiles_of(pv, bb, WT) * rows : 0;
             int64_t all;
             pre = base + block_scan(mine, scan_buf, &all);
             base += all;
@@ -241,11 +271,20 @@ k_decode(const PagedView pv, const DecodeArgs a) {
     __syncthreads();
     int b = s_b;
     Visible vis = visible_of(pv, b);
-    int nt = (vis.count + per_tile - 1) / per_tile;
+    int nt = (vis.tiles + WT - 1) / WT;
     int row = (int)((at - s_before) / nt), tile = (int)((at - s_before) % nt);
 
-    const uint32_t sm = smem_addr(smem) + (uint32_t)(warp * C::WARP_BYTES);
     const uint32_t row_bytes = (uint32_t)(pv.H * pv.Dh);
+    // Byte of a unit where chunk c (16 bytes) of row r lies: 128-byte rows (two
+    // blocks of them for 256), 64-byte rows, in TMA's swizzle of the same width.
+    auto at_chunk = [](int r, int c) -> uint32_t {
+        if (DH == 64) return (uint32_t)(r * 64 + ((c ^ (r >> 1)) & 3) * 16);
+        return (uint32_t)((c >> 3) * 4096 + r * 128 + ((c ^ r) & 7) * 16);
+    };
+    // chunk of a K row that lane t takes as its c-th: even and odd rows then meet different banks
+    auto k_chunk = [](int t, int c) { return DH == 64 ? t : (c >> 1) * 8 + 2 * t + (c & 1); };
+    int fill = 0, read = 0;                   // units of the ring to copy into and to read
+    uint32_t phase = 0;                       // parity of the unit to read
 
     while (true) {
         const int tile_end = (int)min((int64_t)nt, tile + (end - at));
@@ -262,7 +301,7 @@ k_decode(const PagedView pv, const DecodeArgs a) {
             uint32_t mx = 0;
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
-                const int d0 = 16 * (t + 4 * c);
+                const int d0 = 16 * k_chunk(t, c);
                 const bool live = gi < a.G && d0 < pv.Dh;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -301,56 +340,63 @@ k_decode(const PagedView pv, const DecodeArgs a) {
             l[x][0] = l[x][1] = 0.0f;
         }
 
-        const uint8_t *kh = pv.kc + (int64_t)h * pv.Dh + 16 * t, *vhp = pv.vc + (int64_t)h * pv.Dh + VB * g;
+        const uint8_t *kh = pv.kc + (int64_t)h * pv.Dh + 16 * t, *vhp = pv.vc + (int64_t)h * pv.Dh + 16 * t;
         const float *ksh = pv.ks + h, *vsh = pv.vs + h;
         const int ntile = tile_end - tile;
-        // index of this lane's position in the tile whose copies come next, and its slot
-        int fetch = (tile * WT + wt) * kTile + lane;
-        const int fetch_end = tile_end * WT * kTile + lane;        // tiles from there on are not this run's
-        auto slot_at = [&](int i) { return i < vis.count ? pv.slot(b, vis.position(i)) : -1; };
-        int slot = slot_at(fetch);
-        uint32_t fill = sm, read = sm;        // units of the ring to copy into and to read
-        auto issue_k = [&] {                  // K of the next tile
-            if (fetch < fetch_end) {          // the same for all lanes
-                const uint32_t live = __ballot_sync(0xFFFFFFFFu, slot >= 0);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int s = __shfl_sync(0xFFFFFFFFu, slot, g + 8 * r);
-                    const uint8_t *src = kh + (uint64_t)(uint32_t)max(s, 0) * row_bytes;
-#pragma unroll
-                    for (int c = 0; c < KC; ++c)
-                        cp_async<16>(fill + (uint32_t)(((r * KC + c) * 32 + lane) * 16), src + 64 * c,
-                                     s >= 0 && 16 * (t + 4 * c) < pv.Dh);
-                }
-                cp_async<4>(fill + 32 * DH + 4 * lane, ksh + (uint64_t)(uint32_t)max(slot, 0) * (uint32_t)pv.H, slot >= 0);
-                if (lane == 0)
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(fill + 32 * DH + 128), "r"(live) : "memory");
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            fill = fill + C::UNIT == sm + C::WARP_BYTES ? sm : fill + C::UNIT;
+        // The tile whose copies come next: this lane's position in it, its slot and whether it is visible.
+        int fetch = tile, slot = -1;
+        bool live = false;
+        auto look_up = [&] {
+            const int i = fetch * WT + wt;
+            const int j = i < vis.tiles ? vis.position(i) + lane : vis.n;
+            slot = j < vis.n ? pv.slot(b, j) : -1;
+            live = slot >= 0 && vis.sees(j);
         };
-        auto issue_v = [&] {                  // V of the same tile; then the next tile's slots
-            if (fetch < fetch_end) {
+        // K or V of that tile into the next unit
+        auto issue = [&](const CUtensorMap *map, const uint8_t *codes, const float *scales, bool is_k) {
+            if (fetch < tile_end) {           // the same for all lanes
+                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, live);
+                const uint32_t dst = data + (uint32_t)(fill * C::UNIT), ax = aux + (uint32_t)(fill * C::AUX);
+                if constexpr (TMA) {
+                    const uint32_t bar = bars + 8 * fill;
+                    if (lane == 0) mbar_expect_tx(bar, C::UNIT);
+                    if ((lane & (a.box - 1)) == 0) {
+                        // a box without a visible row starts past the last slot: zeros, and nothing is read
+                        const bool any = (mask >> lane) & (0xFFFFFFFFu >> (32 - a.box));
+                        const int z = any && slot >= 0 ? slot : (int)(pv.bs.d * (uint32_t)pv.num_blocks);
+                        tma_load_3d(dst + (uint32_t)(lane * (DH == 64 ? 64 : 128)), map, bar, 0, h, z);
+                        if (DH == 256) tma_load_3d(dst + 4096u + (uint32_t)(lane * 128), map, bar, 128, h, z);
+                    }
+                } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int s = __shfl_sync(0xFFFFFFFFu, slot, 2 * t + (e & 1) + 4 * (e & 2) + 4 * (e & 4));
-                    const uint8_t *src = vhp + (uint64_t)(uint32_t)max(s, 0) * row_bytes;
-                    if constexpr (VB == 8) {
-                        cp_async<8>(fill + (uint32_t)((e * 32 + lane) * 8), src, s >= 0 && 8 * g < pv.Dh);
-                    } else {
+                    for (int r = 0; r < 4; ++r) {
+                        const int s = __shfl_sync(0xFFFFFFFFu, live ? slot : -1, g + 8 * r);
+                        const uint8_t *src = codes + (uint64_t)(uint32_t)max(s, 0) * row_bytes;
 #pragma unroll
-                        for (int c = 0; c < VB / 16; ++c)
-                            cp_async<16>(fill + (uint32_t)(((e * (VB / 16) + c) * 32 + lane) * 16), src + 16 * c,
-                                         s >= 0 && VB * g + 16 * c < pv.Dh);
+                        for (int c = 0; c < KC; ++c)
+                            cp_async<16>(dst + at_chunk(g + 8 * r, t + 4 * c), src + 64 * c,
+                                         s >= 0 && 16 * (t + 4 * c) < pv.Dh);
                     }
                 }
-                cp_async<4>(fill + 32 * DH + 4 * lane, vsh + (uint64_t)(uint32_t)max(slot, 0) * (uint32_t)pv.H, slot >= 0);
+                cp_async<4>(ax + 4 * lane, scales + (uint64_t)(uint32_t)max(slot, 0) * (uint32_t)pv.H, live);
+                if (is_k && lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(ax + 128), "r"(mask) : "memory");
+                fill = fill + 1 == C::UNITS ? 0 : fill + 1;
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
-            fill = fill + C::UNIT == sm + C::WARP_BYTES ? sm : fill + C::UNIT;
-            fetch += WT * kTile;
-            slot = slot_at(fetch);
         };
+        auto issue_k = [&] { issue(&tmK, kh, ksh, true); };
+        auto issue_v = [&] {
+            issue(&tmV, vhp, vsh, false);
+            ++fetch;
+            look_up();
+        };
+        auto next_read = [&] {
+            if (++read == C::UNITS) {
+                read = 0;
+                phase ^= 1u;
+            }
+        };
+        look_up();
         // the ring's last unit is filled when the one that was read before it is done with
 #pragma unroll
         for (int u = 0; u < C::UNITS - 1; ++u) {
@@ -359,10 +405,11 @@ k_decode(const PagedView pv, const DecodeArgs a) {
 
         for (int k = 0; k < ntile; ++k) {
             asm volatile("cp.async.wait_group %0;" ::"n"(C::UNITS - 2) : "memory");
-            __syncwarp();                     // the other lanes' scales; and the unit read before is done with
+            __syncwarp();                     // the other lanes' copies; and the unit read before is done with
             if constexpr (C::UNITS % 2) issue_k(); else issue_v();
-            uint32_t live;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(live) : "r"(read + 32 * DH + 128));
+            uint32_t un = data + (uint32_t)(read * C::UNIT), ax = aux + (uint32_t)(read * C::AUX), seen;
+            if constexpr (TMA) wait_bar(bars + 8 * read, phase, &s_abort, kErrProducer);
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(seen) : "r"(ax + 128));
 
             // ---- S^T = K Q^T, 16 positions at a time
             float s[2][NT][4];
@@ -372,8 +419,8 @@ k_decode(const PagedView pv, const DecodeArgs a) {
                 for (int x = 0; x < NT; ++x) s[y][x][0] = s[y][x][1] = s[y][x][2] = s[y][x][3] = 0.0f;
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
-                    const uint4 k0 = lds128(read + (uint32_t)(((2 * y * KC + c) * 32 + lane) * 16));
-                    const uint4 k1 = lds128(read + (uint32_t)((((2 * y + 1) * KC + c) * 32 + lane) * 16));
+                    const uint4 k0 = lds128(un + at_chunk(16 * y + g, k_chunk(t, c)));
+                    const uint4 k1 = lds128(un + at_chunk(16 * y + g + 8, k_chunk(t, c)));
                     const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -389,8 +436,8 @@ k_decode(const PagedView pv, const DecodeArgs a) {
             bool up = false;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                const float dk0 = lds_f(read + 32 * DH + 4 * (16 * y + g));
-                const float dk1 = lds_f(read + 32 * DH + 4 * (16 * y + g + 8));
+                const float dk0 = lds_f(ax + 4 * (16 * y + g));
+                const float dk1 = lds_f(ax + 4 * (16 * y + g + 8));
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
 #pragma unroll
@@ -400,25 +447,26 @@ k_decode(const PagedView pv, const DecodeArgs a) {
                     }
                 }
             }
-            if (live != 0xFFFFFFFFu) {
+            if (seen != 0xFFFFFFFFu) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
 #pragma unroll
                     for (int x = 0; x < NT; ++x) {
-                        if (!((live >> (16 * y + g)) & 1u)) s[y][x][0] = s[y][x][1] = -INFINITY;
-                        if (!((live >> (16 * y + g + 8)) & 1u)) s[y][x][2] = s[y][x][3] = -INFINITY;
+                        if (!((seen >> (16 * y + g)) & 1u)) s[y][x][0] = s[y][x][1] = -INFINITY;
+                        if (!((seen >> (16 * y + g + 8)) & 1u)) s[y][x][2] = s[y][x][3] = -INFINITY;
                     }
             }
             if (a.logits) {
-                const int i0 = ((tile + k) * WT + wt) * kTile + g;
-                float *lp = a.logits + (((int64_t)b * VH + vh) * a.vis_max + i0) * C::COLS + 2 * t;
+                const int i0 = (tile + k) * WT + wt;
+                float *lp = a.logits + (((int64_t)b * VH + vh) * a.vis_max + (int64_t)i0 * kTile + g) * C::COLS + 2 * t;
+                if (i0 < vis.tiles) {
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
+                    for (int y = 0; y < 4; ++y)
 #pragma unroll
-                    for (int x = 0; x < NT; ++x)
-                        if (i0 + 8 * y < vis.count)
+                        for (int x = 0; x < NT; ++x)
                             *reinterpret_cast<float2 *>(lp + 8 * y * C::COLS + 8 * x) =
                                 make_float2(s[y / 2][x][2 * (y & 1)], s[y / 2][x][2 * (y & 1) + 1]);
+                }
             }
             float mx[NT][2];
 #pragma unroll
@@ -456,15 +504,18 @@ k_decode(const PagedView pv, const DecodeArgs a) {
                         s[y][x][e] = exp2_fast(s[y][x][e] - m[x][e & 1]);
                         l[x][e & 1] += s[y][x][e];
                     }
-            read = read + C::UNIT == sm + C::WARP_BYTES ? sm : read + C::UNIT;
+            next_read();
 
             asm volatile("cp.async.wait_group %0;" ::"n"(C::UNITS - 2) : "memory");
             __syncwarp();
             if constexpr (C::UNITS % 2) issue_v(); else issue_k();
+            un = data + (uint32_t)(read * C::UNIT);
+            ax = aux + (uint32_t)(read * C::AUX);
+            if constexpr (TMA) wait_bar(bars + 8 * read, phase, &s_abort, kErrProducer);
             // ---- the power of two that V's scales are held against
             float dv[4];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) dv[y] = lds_f(read + 32 * DH + 4 * (8 * y + g));
+            for (int y = 0; y < 4; ++y) dv[y] = lds_f(ax + 4 * (8 * y + g));
             const float dmax = fmaxf(fmaxf(fabsf(dv[0]), fabsf(dv[1])), fmaxf(fabsf(dv[2]), fabsf(dv[3])));
             if (__any_sync(0xFFFFFFFFu, dmax > vcap && dmax < INFINITY)) {
                 const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, dmax < INFINITY ? __float_as_uint(dmax) : 0u);
@@ -489,7 +540,26 @@ k_decode(const PagedView pv, const DecodeArgs a) {
                     pb[y][x][1] = transpose8x8(pack_f16x2(s[y][x][2] * f1, s[y][x][3] * f1));
                 }
             }
-            // ---- O^T += V^T P^T
+            // ---- O^T += V^T P^T.  A weight of zero does not hide what a slot that is not visible holds (it
+            // may be a NaN code): such rows of a box become zeros, each by the lane that reads it next.
+            if (TMA && seen != 0xFFFFFFFFu) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int r = 2 * t + (e & 1) + 4 * (e & 2) + 4 * (e & 4);
+                    if (!((seen >> r) & 1u)) {
+                        if constexpr (VB == 8) {
+                            asm volatile("st.shared.v2.u32 [%0], {%1,%1};" ::"r"(un + at_chunk(r, g >> 1) + 8 * (g & 1)),
+                                         "r"(0) : "memory");
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < VB / 16; ++c)
+                                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(un + at_chunk(r, 8 * c + g)),
+                                             "r"(0) : "memory");
+                        }
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the unit's next copy comes by TMA
+            }
 #pragma unroll
             for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -497,11 +567,12 @@ k_decode(const PagedView pv, const DecodeArgs a) {
                     uint32_t v[4][4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
+                        const int r = 16 * y + 2 * t + (e & 1) + 4 * (e & 2);
                         if constexpr (VB == 8) {
-                            const uint2 w = lds64(read + (uint32_t)(((4 * y + e) * 32 + lane) * 8));
+                            const uint2 w = lds64(un + at_chunk(r, g >> 1) + 8 * (g & 1));
                             v[e][0] = w.x; v[e][1] = w.y;
                         } else {
-                            const uint4 w = lds128(read + (uint32_t)((((4 * y + e) * (VB / 16) + c) * 32 + lane) * 16));
+                            const uint4 w = lds128(un + at_chunk(r, 8 * c + g));
                             v[e][0] = w.x; v[e][1] = w.y; v[e][2] = w.z; v[e][3] = w.w;
                         }
                     }
@@ -519,11 +590,13 @@ k_decode(const PagedView pv, const DecodeArgs a) {
                                 mma16816(o[x][c * 8 + w * 2 + hf], a0, a1, a2, a3, pb[y][x][0], pb[y][x][1]);
                         }
                 }
-            read = read + C::UNIT == sm + C::WARP_BYTES ? sm : read + C::UNIT;
+            next_read();
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
 
         // ---- this run of tiles is done: result, or a part of one
+        // o[..][i] holds the head elements dh_of(i) and the next one
+        auto dh_of = [&](int i) { return VB == 8 ? 8 * g + 2 * i : 128 * (i >> 3) + 16 * g + 2 * (i & 7); };
         const float inv = 1.0f / vscale;
 #pragma unroll
         for (int x = 0; x < NT; ++x)
@@ -550,31 +623,31 @@ k_decode(const PagedView pv, const DecodeArgs a) {
                         const float r = l[x][e] == 0.0f ? 0.0f : inv / l[x][e];
                         const int64_t orow = (int64_t)b * pv.H * a.G + h * a.G + gi;
                         if (g == 0) a.lse[orow] = l[x][e] == 0.0f ? -INFINITY : (m[x][e] + log2f(l[x][e])) * kLn2;
-                        __nv_bfloat16 *op = a.out + orow * pv.Dh + VB * g;
+                        __nv_bfloat16 *op = a.out + orow * pv.Dh;
 #pragma unroll
                         for (int c = 0; c < VB / 8; ++c)
-                            if (VB * g + 8 * c < pv.Dh) {
+                            if (dh_of(4 * c) < pv.Dh) {
                                 uint4 w;
                                 w.x = pack_bf16x2(o[x][4 * c][e] * r, o[x][4 * c][2 + e] * r);
                                 w.y = pack_bf16x2(o[x][4 * c + 1][e] * r, o[x][4 * c + 1][2 + e] * r);
                                 w.z = pack_bf16x2(o[x][4 * c + 2][e] * r, o[x][4 * c + 2][2 + e] * r);
                                 w.w = pack_bf16x2(o[x][4 * c + 3][e] * r, o[x][4 * c + 3][2 + e] * r);
-                                *reinterpret_cast<uint4 *>(op + 8 * c) = w;
+                                *reinterpret_cast<uint4 *>(op + dh_of(4 * c)) = w;
                             }
                     } else {
                         const int pc = hw * C::COLS + col;
                         if (g == 0) *reinterpret_cast<float2 *>(part_ml + 2 * pc) = make_float2(m[x][e], l[x][e]);
-                        float *pp = part + (int64_t)pc * DH + VB * g;
+                        float *pp = part + (int64_t)pc * DH;
 #pragma unroll
                         for (int i = 0; i < MI; i += 2)
-                            *reinterpret_cast<float4 *>(pp + 2 * i) =
+                            *reinterpret_cast<float4 *>(pp + dh_of(i)) =
                                 make_float4(o[x][i][e] * inv, o[x][i][2 + e] * inv, o[x][i + 1][e] * inv,
                                             o[x][i + 1][2 + e] * inv);
                     }
                 }
         } else {
             __syncthreads();                  // every warp's copies have landed and been read
-            float *mine = reinterpret_cast<float *>(smem + (size_t)warp * C::WARP_BYTES);
+            float *mine = reinterpret_cast<float *>(smem + (size_t)warp * C::UNITS * C::UNIT);
 #pragma unroll
             for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -586,7 +659,7 @@ k_decode(const PagedView pv, const DecodeArgs a) {
                     }
 #pragma unroll
                     for (int i = 0; i < MI; ++i)
-                        *reinterpret_cast<float2 *>(mine + col * DH + VB * g + 2 * i) =
+                        *reinterpret_cast<float2 *>(mine + col * DH + dh_of(i)) =
                             make_float2(o[x][i][e] * inv, o[x][i][2 + e] * inv);
                 }
             __syncthreads();
@@ -602,7 +675,7 @@ k_decode(const PagedView pv, const DecodeArgs a) {
                 for (int w = 0; w < WT; ++w) {
                     const float al = exp2_fast(s_m[hh * WT + w][col] - mx);
                     const float4 v = *reinterpret_cast<const float4 *>(
-                        smem + (size_t)(hh * WT + w) * C::WARP_BYTES + (size_t)(col * DH + d) * 4);
+                        smem + (size_t)(hh * WT + w) * C::UNITS * C::UNIT + (size_t)(col * DH + d) * 4);
                     sum = fmaf(s_l[hh * WT + w][col], al, sum);
                     acc.x = fmaf(v.x, al, acc.x); acc.y = fmaf(v.y, al, acc.y);
                     acc.z = fmaf(v.z, al, acc.z); acc.w = fmaf(v.w, al, acc.w);
@@ -619,6 +692,7 @@ k_decode(const PagedView pv, const DecodeArgs a) {
                     *reinterpret_cast<float4 *>(part + (int64_t)pc * DH + d) = acc;
                 }
             }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncthreads();                  // before the next run's copies
         }
 
@@ -630,8 +704,8 @@ k_decode(const PagedView pv, const DecodeArgs a) {
             do {
                 ++b;                          // at < end <= total: another sequence with tiles follows
                 vis = visible_of(pv, b);
-            } while (vis.count == 0);
-            nt = (vis.count + per_tile - 1) / per_tile;
+            } while (vis.tiles == 0);
+            nt = (vis.tiles + WT - 1) / WT;
         }
     }
 }
@@ -648,18 +722,18 @@ k_decode_join(const PagedView pv, const DecodeArgs a, int64_t grid) {
     __shared__ float s_acc[kJoinWarps][DH], s_sum[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int Hq = pv.H * a.G, b = (int)(blockIdx.x / Hq), hq = (int)(blockIdx.x % Hq), h = hq / a.G, gi = hq % a.G;
-    const int WT = kWarps / a.HB, VH = pv.H * a.GC, rows = VH / a.HB, per_tile = kTile * WT;
+    const int WT = kWarps / a.HB, VH = pv.H * a.GC, rows = VH / a.HB;
     const int vh = h * a.GC + gi / COLS, row = vh / a.HB, pc = (vh % a.HB) * COLS + gi % COLS;
     const int64_t orow = (int64_t)b * Hq + hq;
     pdl_wait();
-    const int nt = tiles_of(pv, b, per_tile);
+    const int nt = tiles_of(pv, b, WT);
     if (nt == 0) {
         for (int d = threadIdx.x; d < pv.Dh; d += kJoinWarps * 32) a.out[orow * pv.Dh + d] = __float2bfloat16(0.0f);
         if (threadIdx.x == 0) a.lse[orow] = -INFINITY;
         return;
     }
     int64_t total, before;
-    count_tiles(pv, a.B, per_tile, rows, b, scan_buf, &total, &before);
+    count_tiles(pv, a.B, WT, rows, b, scan_buf, &total, &before);
     const int64_t ncta = min(grid, total);
     const int64_t first = before + (int64_t)row * nt, last = first + nt - 1;
     // CTA c holds the tiles [total * c / ncta, total * (c + 1) / ncta): the one with tile x is the largest c
@@ -712,9 +786,10 @@ k_decode_mass(const PagedView pv, const DecodeArgs a) {
     const int b = (int)blockIdx.z, h = (int)blockIdx.y, VH = pv.H * a.GC;
     pdl_wait();
     const Visible vis = visible_of(pv, b);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < vis.count; i += (int64_t)gridDim.x * 256) {
-        const int j = vis.position((int)i);
-        if (j >= a.ld_mass || pv.slot(b, j) < 0) continue;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)vis.tiles * kTile;
+         i += (int64_t)gridDim.x * 256) {
+        const int j = vis.position((int)(i / kTile)) + (int)(i % kTile);
+        if (!vis.sees(j) || j >= a.ld_mass || pv.slot(b, j) < 0) continue;
         float sum = 0.0f;
         for (int c = 0; c < a.GC; ++c) {
             const float *lp = a.logits + (((int64_t)b * VH + h * a.GC + c) * a.vis_max + i) * COLS;
@@ -756,7 +831,8 @@ DecodePlan decode_plan(int64_t B, int64_t Hq, int64_t H, int64_t Dh, int64_t max
     p.ctas = sms * (p.DH <= 128 && p.NT == 1 ? 2 : 1);
     p.part_bytes = round256((size_t)p.ctas * 2 * p.HB * 8 * p.NT * (p.DH + 2) * 4);
     p.lse_bytes = round256((size_t)(B * Hq) * 4);
-    p.logit_bytes = weights ? round256((size_t)(B * VH) * (size_t)max_context * 8 * p.NT * 4) : 0;
+    const size_t tiles = (size_t)((max_context + kTile - 1) / kTile);
+    p.logit_bytes = weights ? round256((size_t)(B * VH) * tiles * kTile * 8 * p.NT * 4) : 0;
     return p;
 }
 
@@ -773,13 +849,38 @@ cudaError_t grant_smem(K kernel, size_t bytes, std::atomic<uint64_t> &done) {
     return e;
 }
 
+// 3-D map over codes [slots, H, Dh]: boxes of `rows` slots of one head, 64 or
+// 128 bytes wide (a head size in between reads zeros behind its end).
+bool make_map_paged(CUtensorMap *map, const void *codes, const PagedView &pv, int DH, int rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)pv.Dh, (cuuint64_t)pv.H, (cuuint64_t)pv.bs.d * (cuuint64_t)pv.num_blocks};
+    cuuint64_t strides[2] = {(cuuint64_t)pv.Dh, (cuuint64_t)pv.Dh * (cuuint64_t)pv.H};
+    cuuint32_t box[3] = {DH == 64 ? 64u : 128u, 1, (cuuint32_t)rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(codes), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, DH == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT, int DH, int NT, bool TMA>
+cudaError_t launch_main(const PagedView &pv, const DecodeArgs &a, const DecodePlan &p, cudaStream_t s) {
+    using C = Cfg<DH, NT>;
+    static std::atomic<uint64_t> granted{0};
+    cudaError_t e = grant_smem(k_decode<FMT, DH, NT, TMA>, C::SMEM, granted);
+    if (e != cudaSuccess) return e;
+    CUtensorMap tk = {}, tv = {};
+    if (TMA && (!make_map_paged(&tk, pv.kc, pv, DH, a.box) || !make_map_paged(&tv, pv.vc, pv, DH, a.box)))
+        return cudaErrorInvalidValue;
+    return pdl_launch(k_decode<FMT, DH, NT, TMA>, dim3(p.ctas), dim3(kWarps * 32), C::SMEM, s, tk, tv, pv, a);
+}
+
 template <int FMT, int DH, int NT>
 cudaError_t launch_decode(const PagedView &pv, const DecodeArgs &a, const DecodePlan &p, cudaStream_t s) {
     using C = Cfg<DH, NT>;
-    static std::atomic<uint64_t> granted{0};
-    cudaError_t e = grant_smem(k_decode<FMT, DH, NT>, C::SMEM, granted);
-    if (e != cudaSuccess) return e;
-    e = pdl_launch(k_decode<FMT, DH, NT>, dim3(p.ctas), dim3(kWarps * 32), C::SMEM, s, pv, a);
+    // pages that 8 rows do not divide, and a pool without pages, have no boxes
+    cudaError_t e = pv.bs.d % 8 == 0 && pv.num_blocks > 0 ? launch_main<FMT, DH, NT, true>(pv, a, p, s)
+                                                          : launch_main<FMT, DH, NT, false>(pv, a, p, s);
     if (e != cudaSuccess) return e;
     e = pdl_launch(k_decode_join<DH, C::COLS>, dim3((unsigned)(a.B * (int64_t)pv.H * a.G)), dim3(kJoinWarps * 32), 0, s, pv, a,
                    (int64_t)p.ctas);
@@ -839,13 +940,15 @@ extern "C" fp8_status fp8_paged_attention_decode(
     a.GC = p.GC;
     a.HB = p.HB;
     a.scale = softmax_scale;
+    a.box = block_size % 32 == 0 ? 32 : block_size % 16 == 0 ? 16 : 8;
     a.out = (__nv_bfloat16 *)out_bf16;
     a.part = (float *)ws;
     a.lse = lse ? lse : (float *)(ws + p.part_bytes);
     if (mass && ld_mass > 0 && context > 0) {
         a.logits = (float *)(ws + p.part_bytes + p.lse_bytes);
-        a.vis_max = window > 0 ? std::min<int64_t>(context, (int64_t)pv.window + pv.sinks) : context;
-        if (pv.window == 0) a.vis_max = context;
+        // whole tiles: at most one begun for the sinks and two for the window
+        a.vis_max = (context + kTile - 1) / kTile * kTile;
+        if (pv.window > 0) a.vis_max = std::min<int64_t>(a.vis_max, (int64_t)pv.window + pv.sinks + 3 * kTile);
         a.mass = mass;
         a.ld_mass = ld_mass;
         a.decay = mass_decay;
@@ -861,4 +964,16 @@ extern "C" fp8_status fp8_paged_attention_decode(
     else FP8Q_DECODE(256, 1);
 #undef FP8Q_DECODE
     return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+}
+
+// This file's device error word (fp8_device_error reads it with the others').
+fp8_status fp8q_decode_device_error(uint32_t *out, int clear) {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_gemm_error, sizeof(v)) != cudaSuccess) return FP8_ERR_CUDA;
+    *out = v;
+    if (clear) {
+        const unsigned int z = 0;
+        if (cudaMemcpyToSymbol(g_gemm_error, &z, sizeof(z)) != cudaSuccess) return FP8_ERR_CUDA;
+    }
+    return FP8_OK;
 }
