@@ -42,7 +42,6 @@ using namespace fp8q;
 
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kTile = 32;                    // positions per warp and step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.0e38f;           // before the first logit; below every finite logit that matters
@@ -57,6 +56,7 @@ struct DecodeArgs {
     __nv_bfloat16 *out;
     float *lse;              // [B, Hq]
     float *part;             // two parts per CTA
+    int2 *span;              // [B, rows]: first and last CTA of each row with tiles
     float *logits;           // weights' scratch [B, H * GC, vis_max, 8 * NT] (log2 units), or nullptr
     int64_t vis_max;
     float *mass;
@@ -70,11 +70,11 @@ struct DecodeArgs {
 // is 134 KiB per SM, more than the HBM rate needs at its latency.
 template <int DH, int NT>
 struct Cfg {
+    static constexpr int WARPS = (DH <= 128 && NT == 1) ? 16 : 8;   // 128 registers a thread, or 255
     static constexpr int UNIT = 32 * DH, AUX = 128 + 16;
-    static constexpr int MIN_CTAS = (DH <= 128 && NT == 1) ? 2 : 1;
     static constexpr int UNITS = DH == 64 ? 6 : DH == 128 ? (NT == 1 ? 3 : 6) : 3;
-    static constexpr int AUX_OFF = kWarps * UNITS * UNIT, BAR_OFF = AUX_OFF + kWarps * UNITS * AUX;
-    static constexpr size_t SMEM = 1024 + BAR_OFF + kWarps * UNITS * 8;
+    static constexpr int AUX_OFF = WARPS * UNITS * UNIT, BAR_OFF = AUX_OFF + WARPS * UNITS * AUX;
+    static constexpr size_t SMEM = 1024 + BAR_OFF + WARPS * UNITS * 8;
     static constexpr int COLS = 8 * NT;                  // query heads per chunk
     static_assert(UNITS * UNIT >= COLS * DH * 4, "the warps' results are merged in the pipeline's memory");
 };
@@ -110,12 +110,15 @@ __device__ __forceinline__ float lds_f(uint32_t a) {
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
     return v;
 }
+// Four codes -> two fp16 pairs (exact).
 template <int FMT>
-__device__ __forceinline__ uint32_t to_f16x2(uint32_t c) {   // the two codes in the low half (exact)
-    uint32_t h;
-    if (FMT == FP8_E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-    else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-    return h;
+__device__ __forceinline__ void to_f16x4(uint32_t c, uint32_t &lo, uint32_t &hi) {
+    if (FMT == FP8_E4M3)
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(c));
+    else
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e5m2x2 %0, l;\n\tcvt.rn.f16x2.e5m2x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(c));
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
@@ -187,27 +190,24 @@ __device__ int64_t block_scan(int64_t v, int64_t *buf, int64_t *total) {   // ex
     *total = all;
     return base + x - v;
 }
-// Block-wide: the tiles of all sequences, and those of the sequences before `b`.
-__device__ void count_tiles(const PagedView &pv, int B, int WT, int rows, int b, int64_t *buf, int64_t *total,
-                            int64_t *before) {
-    int64_t all = 0, pre = 0;
-    for (int i = threadIdx.x; i < B; i += blockDim.x) {
-        const int64_t n = (int64_t)tiles_of(pv, i, WT) * rows;
-        all += n;
-        if (i < b) pre += n;
-    }
-    block_scan(pre, buf, before);
-    block_scan(all, buf, total);
+// Block-wide: the tiles of all sequences.
+__device__ int64_t count_tiles(const PagedView &pv, int B, int WT, int rows, int64_t *buf) {
+    int64_t all = 0, total;
+    for (int i = threadIdx.x; i < B; i += blockDim.x) all += (int64_t)tiles_of(pv, i, WT) * rows;
+    block_scan(all, buf, &total);
+    return total;
 }
+
 // First tile of CTA c of n when `total` tiles are dealt out evenly.
 __device__ __forceinline__ int64_t deal(int64_t total, int64_t n, int64_t c) { return total * c / n; }
 
 // TMA: boxes of a.box rows, which divides the page size; otherwise cp.async.
 template <int FMT, int DH, int NT, bool TMA>
-__global__ void __launch_bounds__(kWarps * 32, Cfg<DH, NT>::MIN_CTAS)
+__global__ void __launch_bounds__(Cfg<DH, NT>::WARPS * 32, 1)
 k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedView pv,
          const DecodeArgs a) {
     using C = Cfg<DH, NT>;
+    constexpr int kWarps = C::WARPS;
     constexpr int KC = DH / 64;              // 16-byte chunks of a K row per lane
     constexpr int VB = DH / 8;               // V bytes of a position per lane
     constexpr int KS = DH / 16;              // k steps of K Q^T
@@ -239,12 +239,12 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
     pdl_trigger();
 
     // the first of this CTA's tiles: its sequence, and the tiles before that
-    int64_t total, unused;
+    int64_t total;
     int64_t mine = 0;
     if (a.B <= kWarps * 32) {
         if (threadIdx.x < a.B) mine = (int64_t)tiles_of(pv, threadIdx.x, WT) * rows;
     } else {
-        count_tiles(pv, a.B, WT, rows, 0, scan_buf, &total, &unused);
+        total = count_tiles(pv, a.B, WT, rows, scan_buf);
     }
     int64_t pre = 0;
     if (a.B <= kWarps * 32) pre = block_scan(mine, scan_buf, &total);
@@ -343,13 +343,19 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
         const uint8_t *kh = pv.kc + (int64_t)h * pv.Dh + 16 * t, *vhp = pv.vc + (int64_t)h * pv.Dh + 16 * t;
         const float *ksh = pv.ks + h, *vsh = pv.vs + h;
         const int ntile = tile_end - tile;
-        // The tile whose copies come next: this lane's position in it, its slot and whether it is visible.
-        int fetch = tile, slot = -1;
+        // The tile whose copies come next: this lane's position in it, its slot and whether it is visible.  The
+        // page id is loaded half a tile before it is looked at.
+        int fetch = tile, j = 0, blk = -1, slot = -1;
         bool live = false;
         auto look_up = [&] {
             const int i = fetch * WT + wt;
-            const int j = i < vis.tiles ? vis.position(i) + lane : vis.n;
-            slot = j < vis.n ? pv.slot(b, j) : -1;
+            j = i < vis.tiles ? vis.position(i) + lane : vis.n;
+            blk = j < vis.n ? __ldg(pv.table + (int64_t)b * pv.max_blocks + pv.bs.div((uint32_t)j)) : -1;
+        };
+        auto look_at = [&] {
+            slot = blk >= 0 && blk < pv.num_blocks
+                       ? (int)((uint32_t)blk * pv.bs.d + ((uint32_t)j - pv.bs.div((uint32_t)j) * pv.bs.d))
+                       : -1;
             live = slot >= 0 && vis.sees(j);
         };
         // K or V of that tile into the next unit
@@ -384,7 +390,10 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto issue_k = [&] { issue(&tmK, kh, ksh, true); };
+        auto issue_k = [&] {
+            look_at();
+            issue(&tmK, kh, ksh, true);
+        };
         auto issue_v = [&] {
             issue(&tmV, vhp, vsh, false);
             ++fetch;
@@ -424,8 +433,9 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
                     const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t a0 = to_f16x2<FMT>(w0[i]), a2 = to_f16x2<FMT>(w0[i] >> 16);
-                        const uint32_t a1 = to_f16x2<FMT>(w1[i]), a3 = to_f16x2<FMT>(w1[i] >> 16);
+                        uint32_t a0, a1, a2, a3;
+                        to_f16x4<FMT>(w0[i], a0, a2);
+                        to_f16x4<FMT>(w1[i], a1, a3);
 #pragma unroll
                         for (int x = 0; x < NT; ++x)
                             mma16816(s[y][x], a0, a1, a2, a3, qf[x][c * 4 + i][0], qf[x][c * 4 + i][1]);
@@ -583,8 +593,9 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
                             const uint32_t sel = hf ? 0x7362u : 0x5140u;
                             const uint32_t xx = __byte_perm(v[0][w], v[1][w], sel);
                             const uint32_t yy = __byte_perm(v[2][w], v[3][w], sel);
-                            const uint32_t a0 = to_f16x2<FMT>(xx), a1 = to_f16x2<FMT>(xx >> 16);
-                            const uint32_t a2 = to_f16x2<FMT>(yy), a3 = to_f16x2<FMT>(yy >> 16);
+                            uint32_t a0, a1, a2, a3;
+                            to_f16x4<FMT>(xx, a0, a1);
+                            to_f16x4<FMT>(yy, a2, a3);
 #pragma unroll
                             for (int x = 0; x < NT; ++x)
                                 mma16816(o[x][c * 8 + w * 2 + hf], a0, a1, a2, a3, pb[y][x][0], pb[y][x][1]);
@@ -609,6 +620,12 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
                 l[x][e] = v;
             }
         const bool whole = tile == 0 && tile_end == nt;
+        if (tile == 0 && threadIdx.x == 0) {
+            // CTA c holds the tiles [total * c / ncta, total * (c + 1) / ncta): the one with tile x is the largest c
+            // with total * c / ncta <= x, that is c <= (x * ncta + ncta - 1) / total
+            const int64_t last = whole ? blockIdx.x : ((at + nt - 1) * ncta + ncta - 1) / total;
+            a.span[(int64_t)b * rows + row] = make_int2(blockIdx.x, (int)last);
+        }
         float *part = a.part + ((int64_t)blockIdx.x * 2 + (tile == 0 ? 1 : 0)) * a.HB * C::COLS * (DH + 2);
         // column c of head hw: DH sums, then (max, sum) behind all columns' sums
         float *part_ml = part + (int64_t)a.HB * C::COLS * DH;
@@ -711,71 +728,80 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
 }
 
 // Joins the parts of the rows that more than one CTA worked on, and writes the
-// results of queries that see nothing.  One CTA per (sequence, query head):
-// a warp per part, a lane per DH / 32 elements.
-constexpr int kJoinWarps = 8;
+// results of queries that see nothing.  One CTA per (sequence, query head, 32
+// head elements): 8 lanes read 128 bytes of a part, so a warp has 4 parts in
+// each of 8 loads and a row that every CTA has a part of takes two rounds.
+constexpr int kJoinWarps = 4;
 template <int DH, int COLS>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-k_decode_join(const PagedView pv, const DecodeArgs a, int64_t grid) {
-    constexpr int E = DH / 32;
-    __shared__ int64_t scan_buf[kJoinWarps];
-    __shared__ float s_acc[kJoinWarps][DH], s_sum[kJoinWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int Hq = pv.H * a.G, b = (int)(blockIdx.x / Hq), hq = (int)(blockIdx.x % Hq), h = hq / a.G, gi = hq % a.G;
-    const int WT = kWarps / a.HB, VH = pv.H * a.GC, rows = VH / a.HB;
-    const int vh = h * a.GC + gi / COLS, row = vh / a.HB, pc = (vh % a.HB) * COLS + gi % COLS;
+k_decode_join(const PagedView pv, const DecodeArgs a) {
+    constexpr int SL = DH / 32, R = 4 * kJoinWarps, U = 8;
+    __shared__ float4 s_acc[R][8];
+    __shared__ float s_sum[R], s_max[R];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> 3, q4 = lane & 7, r = warp * 4 + sub;
+    const int Hq = pv.H * a.G, sl = (int)(blockIdx.x % SL), b = (int)(blockIdx.x / SL / Hq);
+    const int hq = (int)(blockIdx.x / SL % Hq), h = hq / a.G, gi = hq % a.G;
+    const int rows = pv.H * a.GC / a.HB, vh = h * a.GC + gi / COLS, row = vh / a.HB;
+    const int pc = (vh % a.HB) * COLS + gi % COLS;
     const int64_t orow = (int64_t)b * Hq + hq;
     pdl_wait();
-    const int nt = tiles_of(pv, b, WT);
-    if (nt == 0) {
-        for (int d = threadIdx.x; d < pv.Dh; d += kJoinWarps * 32) a.out[orow * pv.Dh + d] = __float2bfloat16(0.0f);
-        if (threadIdx.x == 0) a.lse[orow] = -INFINITY;
+    if (visible_of(pv, b).tiles == 0) {
+        if (threadIdx.x < 32 && 32 * sl + lane < pv.Dh) a.out[orow * pv.Dh + 32 * sl + lane] = __float2bfloat16(0.0f);
+        if (threadIdx.x == 0 && sl == 0) a.lse[orow] = -INFINITY;
         return;
     }
-    int64_t total, before;
-    count_tiles(pv, a.B, WT, rows, b, scan_buf, &total, &before);
-    const int64_t ncta = min(grid, total);
-    const int64_t first = before + (int64_t)row * nt, last = first + nt - 1;
-    // CTA c holds the tiles [total * c / ncta, total * (c + 1) / ncta): the one with tile x is the largest c
-    // with total * c / ncta <= x, that is c <= (x * ncta + ncta - 1) / total
-    const int64_t c0 = (first * ncta + ncta - 1) / total, c1 = (last * ncta + ncta - 1) / total;
-    if (c0 == c1) return;
+    const int2 span = a.span[(int64_t)b * rows + row];
+    if (span.x == span.y || 32 * sl >= pv.Dh) return;
+    // the row's tile 0 is in the first CTA, whose part is the second of its two; the others' is their first
     const int64_t stride = (int64_t)a.HB * COLS * (DH + 2), ml = (int64_t)a.HB * COLS * DH + 2 * pc;
-    // the row's tile 0 is in c0, whose part is the second of its two; the others' is their first
-    auto part = [&](int64_t c) { return a.part + (2 * c + (c == c0 ? 1 : 0)) * stride; };
-    // the largest maximum first (a lane per part), then independent loads of the sums
-    float mx = kNoMax;
-    for (int64_t c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, part(c)[ml]);
+    float mx = kNoMax, sum = 0.0f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int cb = span.x + r; cb <= span.y; cb += U * R) {
+        float2 v[U];
+        float4 o[U];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    float sum = 0.0f, acc[E];
+        for (int i = 0; i < U; ++i) {
+            const int c = min(cb + i * R, span.y);
+            const float *p = a.part + (2 * (int64_t)c + (c == span.x ? 1 : 0)) * stride;
+            v[i] = *reinterpret_cast<const float2 *>(p + ml);
+            o[i] = *reinterpret_cast<const float4 *>(p + (int64_t)pc * DH + 32 * sl + 4 * q4);
+        }
+        float nm = mx;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-    for (int64_t c = c0 + warp; c <= c1; c += kJoinWarps) {
-        const float *p = part(c);
-        const float2 v = *reinterpret_cast<const float2 *>(p + ml);
-        const float be = exp2_fast(v.x - mx);
-        sum = fmaf(v.y, be, sum);
-        const float *o = p + (int64_t)pc * DH + lane * E;
+        for (int i = 0; i < U; ++i) nm = fmaxf(nm, cb + i * R <= span.y ? v[i].x : kNoMax);
+        const float al = exp2_fast(mx - nm);
+        mx = nm;
+        sum *= al;
+        acc.x *= al; acc.y *= al; acc.z *= al; acc.w *= al;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(o[e], be, acc[e]);
+        for (int i = 0; i < U; ++i) {
+            if (cb + i * R > span.y) break;
+            const float be = exp2_fast(v[i].x - nm);
+            sum = fmaf(v[i].y, be, sum);
+            acc.x = fmaf(o[i].x, be, acc.x); acc.y = fmaf(o[i].y, be, acc.y);
+            acc.z = fmaf(o[i].z, be, acc.z); acc.w = fmaf(o[i].w, be, acc.w);
+        }
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-    if (lane == 0) s_sum[warp] = sum;
+    s_acc[r][q4] = acc;
+    if (q4 == 0) {
+        s_max[r] = mx;
+        s_sum[r] = sum;
+    }
     __syncthreads();
+    if (warp > 0) return;
+    mx = s_max[0];
+#pragma unroll
+    for (int w = 1; w < R; ++w) mx = fmaxf(mx, s_max[w]);
     sum = 0.0f;
+    float x = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) sum += s_sum[w];
-    const float r = sum == 0.0f ? 0.0f : 1.0f / sum;
-    for (int d = threadIdx.x; d < pv.Dh; d += kJoinWarps * 32) {
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) v += s_acc[w][d];
-        a.out[orow * pv.Dh + d] = __float2bfloat16(v * r);
+    for (int w = 0; w < R; ++w) {
+        const float al = exp2_fast(s_max[w] - mx);
+        sum = fmaf(s_sum[w], al, sum);
+        x = fmaf(reinterpret_cast<const float *>(s_acc[w])[lane], al, x);
     }
-    if (threadIdx.x == 0) a.lse[orow] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+    if (32 * sl + lane < pv.Dh) a.out[orow * pv.Dh + 32 * sl + lane] = __float2bfloat16(sum == 0.0f ? 0.0f : x / sum);
+    if (lane == 0 && sl == 0) a.lse[orow] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 // mass of the visible positions from the logits and the joined lse.  One
@@ -809,16 +835,17 @@ namespace {
 
 struct DecodePlan {
     int DH, NT, G, GC, HB, ctas, sms;
-    size_t part_bytes, lse_bytes, logit_bytes;
-    size_t total() const { return part_bytes + lse_bytes + logit_bytes; }
+    size_t part_bytes, span_bytes, lse_bytes, logit_bytes;
+    size_t total() const { return part_bytes + span_bytes + lse_bytes + logit_bytes; }
 };
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Groups of up to 8 query heads take one column block, larger ones two (16
 // heads per pass over K and V; a head size of 256 has registers for one).
-// Eight warps share out the largest power of two of heads that divides their
-// number, so that no warp is idle.
+// A CTA's warps share out the largest power of two of heads that divides their
+// number, so that no warp is idle; the warps left per head take turns at its
+// tiles.
 DecodePlan decode_plan(int64_t B, int64_t Hq, int64_t H, int64_t Dh, int64_t max_context, bool weights, int sms) {
     DecodePlan p;
     p.G = (int)(Hq / H);
@@ -826,10 +853,11 @@ DecodePlan decode_plan(int64_t B, int64_t Hq, int64_t H, int64_t Dh, int64_t max
     p.NT = p.G > 8 && p.DH <= 128 ? 2 : 1;
     p.GC = (p.G + 8 * p.NT - 1) / (8 * p.NT);
     const int64_t VH = H * p.GC;
-    p.HB = VH % 8 == 0 ? 8 : VH % 4 == 0 ? 4 : VH % 2 == 0 ? 2 : 1;
-    p.sms = sms;
-    p.ctas = sms * (p.DH <= 128 && p.NT == 1 ? 2 : 1);
+    const int warps = p.DH <= 128 && p.NT == 1 ? 16 : 8;      // Cfg::WARPS
+    for (p.HB = warps; VH % p.HB; p.HB /= 2) {}
+    p.sms = p.ctas = sms;
     p.part_bytes = round256((size_t)p.ctas * 2 * p.HB * 8 * p.NT * (p.DH + 2) * 4);
+    p.span_bytes = round256((size_t)(B * (VH / p.HB)) * 8);
     p.lse_bytes = round256((size_t)(B * Hq) * 4);
     const size_t tiles = (size_t)((max_context + kTile - 1) / kTile);
     p.logit_bytes = weights ? round256((size_t)(B * VH) * tiles * kTile * 8 * p.NT * 4) : 0;
@@ -872,7 +900,7 @@ cudaError_t launch_main(const PagedView &pv, const DecodeArgs &a, const DecodePl
     CUtensorMap tk = {}, tv = {};
     if (TMA && (!make_map_paged(&tk, pv.kc, pv, DH, a.box) || !make_map_paged(&tv, pv.vc, pv, DH, a.box)))
         return cudaErrorInvalidValue;
-    return pdl_launch(k_decode<FMT, DH, NT, TMA>, dim3(p.ctas), dim3(kWarps * 32), C::SMEM, s, tk, tv, pv, a);
+    return pdl_launch(k_decode<FMT, DH, NT, TMA>, dim3(p.ctas), dim3(C::WARPS * 32), C::SMEM, s, tk, tv, pv, a);
 }
 
 template <int FMT, int DH, int NT>
@@ -882,8 +910,8 @@ cudaError_t launch_decode(const PagedView &pv, const DecodeArgs &a, const Decode
     cudaError_t e = pv.bs.d % 8 == 0 && pv.num_blocks > 0 ? launch_main<FMT, DH, NT, true>(pv, a, p, s)
                                                           : launch_main<FMT, DH, NT, false>(pv, a, p, s);
     if (e != cudaSuccess) return e;
-    e = pdl_launch(k_decode_join<DH, C::COLS>, dim3((unsigned)(a.B * (int64_t)pv.H * a.G)), dim3(kJoinWarps * 32), 0, s, pv, a,
-                   (int64_t)p.ctas);
+    e = pdl_launch(k_decode_join<DH, C::COLS>, dim3((unsigned)(a.B * (int64_t)pv.H * a.G * (DH / 32))),
+                   dim3(kJoinWarps * 32), 0, s, pv, a);
     if (e != cudaSuccess || !a.logits) return e;
     // eight CTAs per SM in all, or one per (sequence, head) where there are more of those
     const int64_t pairs = (int64_t)a.B * pv.H, want = std::max<int64_t>(1, 8 * (int64_t)p.sms / pairs);
@@ -943,9 +971,10 @@ extern "C" fp8_status fp8_paged_attention_decode(
     a.box = block_size % 32 == 0 ? 32 : block_size % 16 == 0 ? 16 : 8;
     a.out = (__nv_bfloat16 *)out_bf16;
     a.part = (float *)ws;
-    a.lse = lse ? lse : (float *)(ws + p.part_bytes);
+    a.span = (int2 *)(ws + p.part_bytes);
+    a.lse = lse ? lse : (float *)(ws + p.part_bytes + p.span_bytes);
     if (mass && ld_mass > 0 && context > 0) {
-        a.logits = (float *)(ws + p.part_bytes + p.lse_bytes);
+        a.logits = (float *)(ws + p.part_bytes + p.span_bytes + p.lse_bytes);
         // whole tiles: at most one begun for the sinks and two for the window
         a.vis_max = (context + kTile - 1) / kTile * kTile;
         if (pv.window > 0) a.vis_max = std::min<int64_t>(a.vis_max, (int64_t)pv.window + pv.sinks + 3 * kTile);

@@ -597,8 +597,8 @@ FP8Q_API fp8_status fp8_paged_attention_prefill(
  * for fp8_paged_attention_decode (max_context = max_blocks * block_size and
  * weights != 0 when mass is asked for), tokens = T for
  * fp8_paged_attention_prefill (max_context and weights are then ignored).
- * Apart from 4 bytes per (sequence, query head) and the weights' scratch the
- * size does not grow with B.
+ * Apart from a few bytes per (sequence, query head) and the weights' scratch
+ * the size does not grow with B.
  */
 FP8Q_API fp8_status fp8_paged_attention_workspace_size(int64_t B, int64_t Hq, int64_t H, int64_t Dh,
                                                        int64_t max_context, int weights, int64_t tokens,
