@@ -290,45 +290,6 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
         const int tile_end = (int)min((int64_t)nt, tile + (end - at));
         const int vh = row * a.HB + hw, h = vh / a.GC, chunk = vh % a.GC;
 
-        // ---- Q: this warp's chunk of the group, as fp16 fragments
-        uint32_t qf[NT][KS][2];
-        float cf[NT][2];                      // logit factor (log2 units) of columns 2t, 2t + 1
-#pragma unroll
-        for (int x = 0; x < NT; ++x) {
-            const int gi = chunk * C::COLS + x * 8 + g;
-            const __nv_bfloat16 *qp = a.q + (int64_t)b * a.ld_q + (int64_t)(h * a.G + gi) * pv.Dh;
-            uint4 w[KC][2];
-            uint32_t mx = 0;
-#pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                const int d0 = 16 * k_chunk(t, c);
-                const bool live = gi < a.G && d0 < pv.Dh;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    w[c][e] = live ? *reinterpret_cast<const uint4 *>(qp + d0 + 8 * e) : make_uint4(0, 0, 0, 0);
-                    uint32_t bad = 0;
-                    mx = amax_exact8(mx, w[c][e], bad);       // finite elements only
-                }
-            }
-            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-            const int ex = max((int)(mx >> 7), 14) - 127;     // exponent of the row's largest, at least 2^-113
-            const float up = pow2i(14 - ex);
-#pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                const uint32_t ww[8] = {w[c][0].x, w[c][0].y, w[c][0].z, w[c][0].w,
-                                        w[c][1].x, w[c][1].y, w[c][1].z, w[c][1].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        qf[x][c * 4 + i][e] = pack_f16x2(bf_lo(ww[2 * i + e]) * up, bf_hi(ww[2 * i + e]) * up);
-            }
-            const float f = a.scale * kLog2e * pow2i(ex) * 0x1p-14f;
-            cf[x][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);
-            cf[x][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
-        }
-
         float o[NT][MI][4], m[NT][2], l[NT][2], vscale = 1.0f, vcap = 0.0f;
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
@@ -410,6 +371,45 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
 #pragma unroll
         for (int u = 0; u < C::UNITS - 1; ++u) {
             if (u % 2 == 0) issue_k(); else issue_v();
+        }
+
+        // ---- Q: this warp's chunk of the group, as fp16 fragments
+        uint32_t qf[NT][KS][2];
+        float cf[NT][2];                      // logit factor (log2 units) of columns 2t, 2t + 1
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            const int gi = chunk * C::COLS + x * 8 + g;
+            const __nv_bfloat16 *qp = a.q + (int64_t)b * a.ld_q + (int64_t)(h * a.G + gi) * pv.Dh;
+            uint4 w[KC][2];
+            uint32_t mx = 0;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const int d0 = 16 * k_chunk(t, c);
+                const bool live = gi < a.G && d0 < pv.Dh;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    w[c][e] = live ? *reinterpret_cast<const uint4 *>(qp + d0 + 8 * e) : make_uint4(0, 0, 0, 0);
+                    uint32_t bad = 0;
+                    mx = amax_exact8(mx, w[c][e], bad);       // finite elements only
+                }
+            }
+            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+            const int ex = max((int)(mx >> 7), 14) - 127;     // exponent of the row's largest, at least 2^-113
+            const float up = pow2i(14 - ex);
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const uint32_t ww[8] = {w[c][0].x, w[c][0].y, w[c][0].z, w[c][0].w,
+                                        w[c][1].x, w[c][1].y, w[c][1].z, w[c][1].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        qf[x][c * 4 + i][e] = pack_f16x2(bf_lo(ww[2 * i + e]) * up, bf_hi(ww[2 * i + e]) * up);
+            }
+            const float f = a.scale * kLog2e * pow2i(ex) * 0x1p-14f;
+            cf[x][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);
+            cf[x][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
         }
 
         for (int k = 0; k < ntile; ++k) {
@@ -730,12 +730,12 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
 // Joins the parts of the rows that more than one CTA worked on, and writes the
 // results of queries that see nothing.  One CTA per (sequence, query head, 32
 // head elements): 8 lanes read 128 bytes of a part, so a warp has 4 parts in
-// each of 8 loads and a row that every CTA has a part of takes two rounds.
+// each of 10 loads and one round takes a row that 160 CTAs have a part of.
 constexpr int kJoinWarps = 4;
 template <int DH, int COLS>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 k_decode_join(const PagedView pv, const DecodeArgs a) {
-    constexpr int SL = DH / 32, R = 4 * kJoinWarps, U = 8;
+    constexpr int SL = DH / 32, R = 4 * kJoinWarps, U = 10;
     __shared__ float4 s_acc[R][8];
     __shared__ float s_sum[R], s_max[R];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> 3, q4 = lane & 7, r = warp * 4 + sub;
@@ -745,12 +745,12 @@ k_decode_join(const PagedView pv, const DecodeArgs a) {
     const int pc = (vh % a.HB) * COLS + gi % COLS;
     const int64_t orow = (int64_t)b * Hq + hq;
     pdl_wait();
+    const int2 span = a.span[(int64_t)b * rows + row];          // not looked at where the row has no tiles
     if (visible_of(pv, b).tiles == 0) {
         if (threadIdx.x < 32 && 32 * sl + lane < pv.Dh) a.out[orow * pv.Dh + 32 * sl + lane] = __float2bfloat16(0.0f);
         if (threadIdx.x == 0 && sl == 0) a.lse[orow] = -INFINITY;
         return;
     }
-    const int2 span = a.span[(int64_t)b * rows + row];
     if (span.x == span.y || 32 * sl >= pv.Dh) return;
     // the row's tile 0 is in the first CTA, whose part is the second of its two; the others' is their first
     const int64_t stride = (int64_t)a.HB * COLS * (DH + 2), ml = (int64_t)a.HB * COLS * DH + 2 * pc;

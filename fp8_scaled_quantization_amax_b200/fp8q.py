@@ -126,27 +126,47 @@ def _dev(t, dtype, what):
         raise ValueError(f"{what}: must be contiguous")
 
 
-def _same_device(first, **others):
-    """Every tensor on the device of `first`: the library runs on that device."""
-    for what, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{what}: on {t.device}, expected {first.device}")
+def _dev_on(index, dtype, **tensors):
+    """_dev() for several tensors of one dtype (None: not given), all on the CUDA device `index`: the library runs
+    there, whatever the current device is."""
+    for what, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != index:
+            _dev(t, dtype, what)
+            raise ValueError(f"{what}: on {t.device}, expected cuda:{index}")
 
 
 def _token_rows(t, what):
-    """bf16 [T, heads, Dh] whose tokens may lie apart (a slice of a fused projection); its token stride."""
+    """bf16 [T, heads, Dh] whose tokens may lie apart (a slice of a fused projection): its device index and token
+    stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{what}: must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{what}: expected {torch.bfloat16}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{what}: expected [tokens, heads, Dh]")
     T, Hq, Dh = t.shape
-    if t.numel() and ((Dh > 1 and t.stride(2) != 1) or (Hq > 1 and t.stride(1) != Dh)):
+    ld, sh, sd = t.stride()
+    if T * Hq * Dh and ((Dh > 1 and sd != 1) or (Hq > 1 and sh != Dh)):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
-    return t.stride(0) if T > 1 else Hq * Dh
+    return t.get_device(), ld if T > 1 else Hq * Dh
+
+
+def _call_on(index, name, stream, *args):
+    """The library function `name` on device `index` and its current stream (or the given one); tensors among the
+    arguments pass as pointers."""
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _call_on(index, name, stream, *args)
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    status = f(*[x.data_ptr() if isinstance(x, torch.Tensor) else x for x in args], stream.cuda_stream)
+    if status:
+        raise Fp8Error(name, status)
 
 
 # ------------------------------------------------------- raw entry points --
@@ -383,37 +403,28 @@ def fp8_paged_kv_gather(cache, scale_cache, block_table, seq_lens, B, max_blocks
 def fp8_paged_attention_decode(q, ld_q, B, Hq, k_cache, k_scale, v_cache, v_scale, H, Dh, block_size, num_blocks, fmt,
                                block_table, seq_lens, max_blocks, window, sinks, softmax_scale, out, lse=None,
                                mass=None, ld_mass=0, mass_decay=1.0, workspace=None, stream=None):
-    _token_rows(q, "q"); _dev(k_cache, torch.uint8, "k_cache"); _dev(v_cache, torch.uint8, "v_cache")
-    _dev(k_scale, torch.float32, "k_scale"); _dev(v_scale, torch.float32, "v_scale")
-    _dev(block_table, torch.int32, "block_table"); _dev(seq_lens, torch.int32, "seq_lens")
-    _dev(out, torch.bfloat16, "out"); _dev(lse, torch.float32, "lse"); _dev(mass, torch.float32, "mass")
-    _dev(workspace, torch.uint8, "workspace")
-    _same_device(q, k_cache=k_cache, k_scale=k_scale, v_cache=v_cache, v_scale=v_scale, block_table=block_table,
-                 seq_lens=seq_lens, out=out, lse=lse, mass=mass, workspace=workspace)
-    with torch.cuda.device(q.device):
-        _check("fp8_paged_attention_decode", lib().fp8_paged_attention_decode(
-            _ptr(q), ld_q, B, Hq, _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), H, Dh, block_size,
-            num_blocks, fmt, _ptr(block_table), _ptr(seq_lens), max_blocks, window, sinks, softmax_scale, _ptr(out),
-            _ptr(lse), _ptr(mass), ld_mass, mass_decay, _ptr(workspace), 0 if workspace is None else workspace.numel(),
-            _stream(stream)))
+    d, _ = _token_rows(q, "q")
+    _dev_on(d, torch.uint8, k_cache=k_cache, v_cache=v_cache, workspace=workspace)
+    _dev_on(d, torch.float32, k_scale=k_scale, v_scale=v_scale, lse=lse, mass=mass)
+    _dev_on(d, torch.int32, block_table=block_table, seq_lens=seq_lens)
+    _dev_on(d, torch.bfloat16, out=out)
+    _call_on(d, "fp8_paged_attention_decode", stream, q, ld_q, B, Hq, k_cache, k_scale, v_cache, v_scale, H, Dh,
+             block_size, num_blocks, fmt, block_table, seq_lens, max_blocks, window, sinks, softmax_scale, out, lse,
+             mass, ld_mass, mass_decay, workspace, 0 if workspace is None else workspace.numel())
 
 
 def fp8_paged_attention_prefill(q, ld_q, T, q_offsets, B, Hq, k_cache, k_scale, v_cache, v_scale, H, Dh, block_size,
                                 num_blocks, fmt, block_table, seq_lens, max_blocks, window, sinks, softmax_scale, out,
                                 lse=None, workspace=None, stream=None):
-    _token_rows(q, "q"); _dev(k_cache, torch.uint8, "k_cache"); _dev(v_cache, torch.uint8, "v_cache")
-    _dev(k_scale, torch.float32, "k_scale"); _dev(v_scale, torch.float32, "v_scale")
-    _dev(q_offsets, torch.int64, "q_offsets"); _dev(block_table, torch.int32, "block_table")
-    _dev(seq_lens, torch.int32, "seq_lens"); _dev(out, torch.bfloat16, "out"); _dev(lse, torch.float32, "lse")
-    _dev(workspace, torch.uint8, "workspace")
-    _same_device(q, q_offsets=q_offsets, k_cache=k_cache, k_scale=k_scale, v_cache=v_cache, v_scale=v_scale,
-                 block_table=block_table, seq_lens=seq_lens, out=out, lse=lse, workspace=workspace)
-    with torch.cuda.device(q.device):
-        _check("fp8_paged_attention_prefill", lib().fp8_paged_attention_prefill(
-            _ptr(q), ld_q, T, _ptr(q_offsets), B, Hq, _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), H,
-            Dh, block_size, num_blocks, fmt, _ptr(block_table), _ptr(seq_lens), max_blocks, window, sinks,
-            softmax_scale, _ptr(out), _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-            _stream(stream)))
+    d, _ = _token_rows(q, "q")
+    _dev_on(d, torch.uint8, k_cache=k_cache, v_cache=v_cache, workspace=workspace)
+    _dev_on(d, torch.float32, k_scale=k_scale, v_scale=v_scale, lse=lse)
+    _dev_on(d, torch.int32, block_table=block_table, seq_lens=seq_lens)
+    _dev_on(d, torch.int64, q_offsets=q_offsets)
+    _dev_on(d, torch.bfloat16, out=out)
+    _call_on(d, "fp8_paged_attention_prefill", stream, q, ld_q, T, q_offsets, B, Hq, k_cache, k_scale, v_cache, v_scale,
+             H, Dh, block_size, num_blocks, fmt, block_table, seq_lens, max_blocks, window, sinks, softmax_scale, out,
+             lse, workspace, 0 if workspace is None else workspace.numel())
 
 
 def fp8_paged_attention_workspace_size(B, Hq, H, Dh, max_context, weights, tokens) -> int:
@@ -426,18 +437,15 @@ def fp8_paged_attention_workspace_size(B, Hq, H, Dh, max_context, weights, token
 def fp8_paged_kv_evict(k_cache, k_scale, v_cache, v_scale, H, Dh, block_size, num_blocks, block_table, seq_lens, B,
                        max_blocks, mass, ld_mass, dst_table, dst_max_blocks, budget, sinks, recent, kept, mass_out,
                        ld_out, lens_out, stream=None):
-    _dev(k_cache, torch.uint8, "k_cache"); _dev(v_cache, torch.uint8, "v_cache")
-    _dev(k_scale, torch.float32, "k_scale"); _dev(v_scale, torch.float32, "v_scale")
-    _dev(block_table, torch.int32, "block_table"); _dev(seq_lens, torch.int32, "seq_lens")
-    _dev(mass, torch.float32, "mass"); _dev(dst_table, torch.int32, "dst_table"); _dev(kept, torch.int32, "kept")
-    _dev(mass_out, torch.float32, "mass_out"); _dev(lens_out, torch.int32, "lens_out")
-    _same_device(k_cache, k_scale=k_scale, v_cache=v_cache, v_scale=v_scale, block_table=block_table,
-                 seq_lens=seq_lens, mass=mass, dst_table=dst_table, kept=kept, mass_out=mass_out, lens_out=lens_out)
-    with torch.cuda.device(k_cache.device):
-        _check("fp8_paged_kv_evict", lib().fp8_paged_kv_evict(
-            _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), H, Dh, block_size, num_blocks,
-            _ptr(block_table), _ptr(seq_lens), B, max_blocks, _ptr(mass), ld_mass, _ptr(dst_table), dst_max_blocks,
-            budget, sinks, recent, _ptr(kept), _ptr(mass_out), ld_out, _ptr(lens_out), _stream(stream)))
+    _dev(k_cache, torch.uint8, "k_cache")
+    d = k_cache.get_device()
+    _dev_on(d, torch.uint8, v_cache=v_cache)
+    _dev_on(d, torch.float32, k_scale=k_scale, v_scale=v_scale, mass=mass, mass_out=mass_out)
+    _dev_on(d, torch.int32, block_table=block_table, seq_lens=seq_lens, dst_table=dst_table, kept=kept,
+            lens_out=lens_out)
+    _call_on(d, "fp8_paged_kv_evict", stream, k_cache, k_scale, v_cache, v_scale, H, Dh, block_size, num_blocks,
+             block_table, seq_lens, B, max_blocks, mass, ld_mass, dst_table, dst_max_blocks, budget, sinks, recent, kept,
+             mass_out, ld_out, lens_out)
 
 
 def fp8_scale_stats(scales, prev, n, seg_offsets, num_segments, jump_ratio, stats, counts, stream=None):
@@ -586,8 +594,8 @@ class PagedKVCache:
 
 
 def _kv_pair(k_cache, v_cache):
-    same = ("fmt", "block_size", "H", "Dh", "num_blocks")
-    if any(getattr(k_cache, a) != getattr(v_cache, a) for a in same):
+    k, v = k_cache, v_cache
+    if (k.fmt, k.block_size, k.H, k.Dh, k.num_blocks) != (v.fmt, v.block_size, v.H, v.Dh, v.num_blocks):
         raise ValueError("the K and V caches must have the same format and shape")
     return (k_cache.cache, k_cache.scale_inv, v_cache.cache, v_cache.scale_inv)
 
@@ -612,7 +620,7 @@ def paged_attention_decode(q, k_cache, v_cache, block_table, seq_lens, window=0,
     paged caches (PagedKVCache of K and of V).  window > 0: only the last `window` positions and the first `sinks`.
     mass [B, H, ld] fp32: becomes mass_decay * mass + each visible token's attention weight, summed over the query
     heads of its KV head.  softmax_scale: Dh ** -0.5 unless given."""
-    ld_q = _token_rows(q, "q")
+    _, ld_q = _token_rows(q, "q")
     B, Hq, Dh = q.shape
     caches = _kv_pair(k_cache, v_cache)
     H = k_cache.H
@@ -639,7 +647,7 @@ def paged_attention_prefill(q, q_offsets, k_cache, v_cache, block_table, seq_len
     """(out [T, Hq, Dh] bf16, lse [T, Hq] fp32): causal attention of the rows q_offsets[b] .. q_offsets[b + 1]
     (int64 [B + 1], device) of q [T, Hq, Dh], the last positions of sequence b, over the paged caches.  Rows that
     belong to no sequence are not written."""
-    ld_q = _token_rows(q, "q")
+    _, ld_q = _token_rows(q, "q")
     T, Hq, Dh = q.shape
     caches = _kv_pair(k_cache, v_cache)
     H = k_cache.H
