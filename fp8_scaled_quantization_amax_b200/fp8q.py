@@ -126,13 +126,15 @@ def _dev(t, dtype, what):
         raise ValueError(f"{what}: must be contiguous")
 
 
-def _dev_on(index, dtype, **tensors):
-    """_dev() for several tensors of one dtype (None: not given), all on the CUDA device `index`: the library runs
-    there, whatever the current device is."""
-    for what, t in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != index:
+def _fits(t, dtype, index):
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+
+
+def _dev_on(index, checks):
+    """_dev() for (tensor or None, dtype, name) triples, all on the CUDA device `index`: the library runs there,
+    whatever the current device is."""
+    for t, dtype, what in checks:
+        if t is not None and not _fits(t, dtype, index):
             _dev(t, dtype, what)
             raise ValueError(f"{what}: on {t.device}, expected cuda:{index}")
 
@@ -155,18 +157,20 @@ def _token_rows(t, what):
     return t.get_device(), ld if T > 1 else Hq * Dh
 
 
-def _call_on(index, name, stream, *args):
-    """The library function `name` on device `index` and its current stream (or the given one); tensors among the
-    arguments pass as pointers."""
-    f = getattr(lib(), name)
+def _call_on(index, name, stream, args):
+    """The library function `name` with `args` and a stream, on device `index` (its current stream unless given)."""
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
-            return _call_on(index, name, stream, *args)
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    status = f(*[x.data_ptr() if isinstance(x, torch.Tensor) else x for x in args], stream.cuda_stream)
+            return _call_on(index, name, stream, args)
+    # the raw handle: building a torch.cuda.Stream object costs 3 us, as much as a launch
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    status = getattr(lib(), name)(*args, raw)
     if status:
         raise Fp8Error(name, status)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 # ------------------------------------------------------- raw entry points --
@@ -404,27 +408,29 @@ def fp8_paged_attention_decode(q, ld_q, B, Hq, k_cache, k_scale, v_cache, v_scal
                                block_table, seq_lens, max_blocks, window, sinks, softmax_scale, out, lse=None,
                                mass=None, ld_mass=0, mass_decay=1.0, workspace=None, stream=None):
     d, _ = _token_rows(q, "q")
-    _dev_on(d, torch.uint8, k_cache=k_cache, v_cache=v_cache, workspace=workspace)
-    _dev_on(d, torch.float32, k_scale=k_scale, v_scale=v_scale, lse=lse, mass=mass)
-    _dev_on(d, torch.int32, block_table=block_table, seq_lens=seq_lens)
-    _dev_on(d, torch.bfloat16, out=out)
-    _call_on(d, "fp8_paged_attention_decode", stream, q, ld_q, B, Hq, k_cache, k_scale, v_cache, v_scale, H, Dh,
-             block_size, num_blocks, fmt, block_table, seq_lens, max_blocks, window, sinks, softmax_scale, out, lse,
-             mass, ld_mass, mass_decay, workspace, 0 if workspace is None else workspace.numel())
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    _dev_on(d, ((k_cache, u8, "k_cache"), (v_cache, u8, "v_cache"), (k_scale, f32, "k_scale"),
+                (v_scale, f32, "v_scale"), (block_table, i32, "block_table"), (seq_lens, i32, "seq_lens"),
+                (out, torch.bfloat16, "out"), (lse, f32, "lse"), (mass, f32, "mass"), (workspace, u8, "workspace")))
+    _call_on(d, "fp8_paged_attention_decode", stream, (
+        _addr(q), ld_q, B, Hq, _addr(k_cache), _addr(k_scale), _addr(v_cache), _addr(v_scale), H, Dh, block_size,
+        num_blocks, fmt, _addr(block_table), _addr(seq_lens), max_blocks, window, sinks, softmax_scale, _addr(out),
+        _addr(lse), _addr(mass), ld_mass, mass_decay, _addr(workspace), 0 if workspace is None else workspace.numel()))
 
 
 def fp8_paged_attention_prefill(q, ld_q, T, q_offsets, B, Hq, k_cache, k_scale, v_cache, v_scale, H, Dh, block_size,
                                 num_blocks, fmt, block_table, seq_lens, max_blocks, window, sinks, softmax_scale, out,
                                 lse=None, workspace=None, stream=None):
     d, _ = _token_rows(q, "q")
-    _dev_on(d, torch.uint8, k_cache=k_cache, v_cache=v_cache, workspace=workspace)
-    _dev_on(d, torch.float32, k_scale=k_scale, v_scale=v_scale, lse=lse)
-    _dev_on(d, torch.int32, block_table=block_table, seq_lens=seq_lens)
-    _dev_on(d, torch.int64, q_offsets=q_offsets)
-    _dev_on(d, torch.bfloat16, out=out)
-    _call_on(d, "fp8_paged_attention_prefill", stream, q, ld_q, T, q_offsets, B, Hq, k_cache, k_scale, v_cache, v_scale,
-             H, Dh, block_size, num_blocks, fmt, block_table, seq_lens, max_blocks, window, sinks, softmax_scale, out,
-             lse, workspace, 0 if workspace is None else workspace.numel())
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    _dev_on(d, ((k_cache, u8, "k_cache"), (v_cache, u8, "v_cache"), (k_scale, f32, "k_scale"),
+                (v_scale, f32, "v_scale"), (q_offsets, torch.int64, "q_offsets"), (block_table, i32, "block_table"),
+                (seq_lens, i32, "seq_lens"), (out, torch.bfloat16, "out"), (lse, f32, "lse"),
+                (workspace, u8, "workspace")))
+    _call_on(d, "fp8_paged_attention_prefill", stream, (
+        _addr(q), ld_q, T, _addr(q_offsets), B, Hq, _addr(k_cache), _addr(k_scale), _addr(v_cache), _addr(v_scale), H,
+        Dh, block_size, num_blocks, fmt, _addr(block_table), _addr(seq_lens), max_blocks, window, sinks, softmax_scale,
+        _addr(out), _addr(lse), _addr(workspace), 0 if workspace is None else workspace.numel()))
 
 
 def fp8_paged_attention_workspace_size(B, Hq, H, Dh, max_context, weights, tokens) -> int:
@@ -439,13 +445,14 @@ def fp8_paged_kv_evict(k_cache, k_scale, v_cache, v_scale, H, Dh, block_size, nu
                        ld_out, lens_out, stream=None):
     _dev(k_cache, torch.uint8, "k_cache")
     d = k_cache.get_device()
-    _dev_on(d, torch.uint8, v_cache=v_cache)
-    _dev_on(d, torch.float32, k_scale=k_scale, v_scale=v_scale, mass=mass, mass_out=mass_out)
-    _dev_on(d, torch.int32, block_table=block_table, seq_lens=seq_lens, dst_table=dst_table, kept=kept,
-            lens_out=lens_out)
-    _call_on(d, "fp8_paged_kv_evict", stream, k_cache, k_scale, v_cache, v_scale, H, Dh, block_size, num_blocks,
-             block_table, seq_lens, B, max_blocks, mass, ld_mass, dst_table, dst_max_blocks, budget, sinks, recent, kept,
-             mass_out, ld_out, lens_out)
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    _dev_on(d, ((v_cache, u8, "v_cache"), (k_scale, f32, "k_scale"), (v_scale, f32, "v_scale"), (mass, f32, "mass"),
+                (mass_out, f32, "mass_out"), (block_table, i32, "block_table"), (seq_lens, i32, "seq_lens"),
+                (dst_table, i32, "dst_table"), (kept, i32, "kept"), (lens_out, i32, "lens_out")))
+    _call_on(d, "fp8_paged_kv_evict", stream, (
+        _addr(k_cache), _addr(k_scale), _addr(v_cache), _addr(v_scale), H, Dh, block_size, num_blocks,
+        _addr(block_table), _addr(seq_lens), B, max_blocks, _addr(mass), ld_mass, _addr(dst_table), dst_max_blocks,
+        budget, sinks, recent, _addr(kept), _addr(mass_out), ld_out, _addr(lens_out)))
 
 
 def fp8_scale_stats(scales, prev, n, seg_offsets, num_segments, jump_ratio, stats, counts, stream=None):
@@ -631,8 +638,8 @@ def paged_attention_decode(q, k_cache, v_cache, block_table, seq_lens, window=0,
         raise ValueError("q, block_table, seq_lens and mass must be of one batch")
     if out is not None and out.shape != q.shape:
         raise ValueError("out must have the shape of q")
-    o = out if out is not None else torch.empty((B, Hq, Dh), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    o = out if out is not None else q.new_empty((B, Hq, Dh))
+    lse = q.new_empty((B, Hq), dtype=torch.float32)
     if workspace is None and B:
         workspace = paged_attention_workspace(B, Hq, H, Dh, mb * k_cache.block_size, mass is not None, 0, q.device)
     fp8_paged_attention_decode(q, ld_q, B, Hq, *caches, H, Dh, k_cache.block_size, k_cache.num_blocks, k_cache.fmt,
@@ -658,8 +665,8 @@ def paged_attention_prefill(q, q_offsets, k_cache, v_cache, block_table, seq_len
         raise ValueError("expected q_offsets [B + 1]")
     if out is not None and out.shape != q.shape:
         raise ValueError("out must have the shape of q")
-    o = out if out is not None else torch.empty((T, Hq, Dh), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    o = out if out is not None else q.new_empty((T, Hq, Dh))
+    lse = q.new_empty((T, Hq), dtype=torch.float32)
     if workspace is None and T:
         workspace = paged_attention_workspace(B, Hq, H, Dh, tokens=T, device=q.device)
     fp8_paged_attention_prefill(q, ld_q, T, q_offsets, B, Hq, *caches, H, Dh, k_cache.block_size, k_cache.num_blocks,
