@@ -1042,6 +1042,7 @@ fp8_status fp8q_mx_device_error(uint32_t *out, int clear);
 fp8_status fp8q_wgrad_device_error(uint32_t *out, int clear);
 fp8_status fp8q_block_device_error(uint32_t *out, int clear);
 fp8_status fp8q_decode_device_error(uint32_t *out, int clear);
+fp8_status fp8q_prefill_device_error(uint32_t *out, int clear);
 
 extern "C" fp8_status fp8_device_error(uint32_t *host_out, int clear) {
     if (!host_out) return FP8_ERR_INVALID_ARG;
@@ -1059,7 +1060,10 @@ extern "C" fp8_status fp8_device_error(uint32_t *host_out, int clear) {
     uint32_t d = 0;
     st = fp8q_decode_device_error(&d, clear);
     if (st != FP8_OK) return st;
-    *host_out = v | w | g | b | d;
+    uint32_t pf = 0;
+    st = fp8q_prefill_device_error(&pf, clear);
+    if (st != FP8_OK) return st;
+    *host_out = v | w | g | b | d | pf;
     if (clear) {
         const unsigned int z = 0;
         if (cudaMemcpyToSymbol(g_gemm_error, &z, sizeof(z)) != cudaSuccess) return FP8_ERR_CUDA;

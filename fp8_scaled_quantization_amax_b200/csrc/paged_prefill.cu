@@ -1,105 +1,956 @@
 // paged_prefill.cu -- causal attention of several new tokens per sequence over
-// the paged FP8 KV cache, read in place.
+// the paged FP8 KV cache (a prompt, a chunk of one, a few drafted tokens).
+//
+// The query heads of a KV head and the new tokens form the rows of one matrix
+// product: row (token, head of the group), 256 rows to a unit of work in two
+// 128-row tiles, so every K and V tile that is read and converted serves 256
+// rows.  Per tile of 128 positions, on tcgen05:
+//   S = Q K^T   both operands fp16 in shared memory, S in TMEM;
+//   softmax     a thread per row, S in its registers; P back to TMEM as fp16;
+//   O += P V    P from TMEM, V from shared memory, O stays in TMEM.
+// E4M3 and E5M2 codes are exact in fp16.  K's row scales multiply the columns
+// of S in fp32; V's are multiplied into the fp16 V (one rounding of 2^-12),
+// against a running power of two of the largest scale so far.  Q's rows are
+// brought to [2^14, 2^15) by a power of two, exact in fp16 above 2^-24 of the
+// row's largest.  The softmax reference only moves when a logit passes it by
+// 2^15 (then to 2^7 below the maximum), so O is seldom rescaled, and weights
+// are exact to 2^-11 down to 2^-21 of the largest in fp16.
+//
+// Warp roles: warp 0 issues the MMAs; warpgroups 1 and 2 are the softmax of the
+// two row tiles (and load Q, rescale O, write results); warpgroup 3 reads the
+// cache through the block table, converts and writes the K and V tiles (two
+// buffers each).  The tensor core alternates between the row tiles, so one
+// tile's softmax runs under the other's products.
+//
+// Split: k_prefill_plan lists the row blocks of all sequences and deals the
+// (row block, head, position tile) triples, laid end to end, to the CTAs in
+// equal runs.  A unit that one CTA covers is written at once; the others leave
+// (O, reference, sum) in the workspace and k_prefill_join adds the parts in the
+// order of the CTAs.
+//
+// What a row must not see is kept out of it whatever it holds: S is masked by
+// selection; V rows of slots that are no live position are written as zeros;
+// and since a weight of zero does not hide a NaN or infinity in V, such values
+// in tiles that only part of the rows see are written as zeros as well, and
+// added to the rows that do see them at the end.
+#include <algorithm>
+#include <atomic>
+
 #include "paged_attn.cuh"
+#include "tc.cuh"
 
 using namespace fp8q;
 
 namespace {
 
-constexpr int kT = 128;       // threads = positions per tile
-constexpr int kMaxDh = 256;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNoMax = -3.0e38f;    // the reference before the first logit
+constexpr float kAbove = 15.0f;       // log2 of how far a logit may pass the reference
+constexpr float kBelow = 7.0f;        // log2 of how far under the maximum it is then set
 
-template <int FMT>
-__device__ __forceinline__ float fp8_to_float(uint8_t c) { return fp8x2_to_float2<FMT>((uint16_t)c).x; }
+struct PrefillArgs {
+    const __nv_bfloat16 *q;
+    int64_t ld_q;
+    const int64_t *q_off;
+    int64_t T;
+    int B, G, ctas;
+    int64_t max_blocks;       // row blocks that the workspace has room for
+    float scale;
+    __nv_bfloat16 *out;
+    float *lse;               // or nullptr
+    float *part;              // two parts per CTA
+    int2 *span;               // per unit: first and last CTA
+    int64_t *hdr;             // {tiles in all, row blocks}
+    int64_t *first_block;     // [B + 1] row blocks before each sequence
+    int2 *block;              // {sequence, row block of it}
+    longlong2 *start;         // per CTA: {row block, tiles before it}
+};
 
-__device__ __forceinline__ float block_reduce(float v, bool is_max, float *buf) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        v = is_max ? fmaxf(v, w) : v + w;
+template <int DH>
+struct Pre {
+    static constexpr int MT = DH <= 128 ? 2 : 1;          // 128-row tiles of a unit
+    static constexpr int KT = DH <= 128 ? 128 : 64;       // positions per tile
+    static constexpr int ROWS = 128 * MT;
+    static constexpr int QB = 128 * DH * 2, KVB = KT * DH * 2;   // bytes of a Q tile, of a K or V buffer
+    static constexpr int META = 8;                        // tiles whose scales and masks are kept
+    static constexpr int OFF_K = MT * QB, OFF_V = OFF_K + 2 * KVB, OFF_M = OFF_V + 2 * KVB;
+    static constexpr int M_DK = 0, M_DV = KT * 4, M_SLOT = KT * 8, M_LIVE = KT * 12, M_MAX = M_LIVE + 16,
+                         M_EXP = M_MAX + 16, M_BYTES = M_EXP + 16;
+    static constexpr int OFF_BAR = OFF_M + META * M_BYTES;
+    static constexpr int NBARS = 8 + 4 * MT + 1;
+    static constexpr size_t SMEM = 1024 + OFF_BAR + NBARS * 8 + 64;
+    static constexpr int S_COL = KT, O_COL = 256;         // TMEM: S of tile i at i * S_COL, O at O_COL + i * DH
+    static constexpr int VC_E4M3 = 6, VC_E5M2 = -1;       // code * scale * 2^(VC - exponent of the largest) < 2^16
+};
+
+constexpr int kThreads = 512;
+// registers per thread: launch pool 128 * 512; MMA warpgroup, softmax, converter
+constexpr int kRegsLaunch = 128, kRegsMma = 56, kRegsSoft = 176, kRegsConv = 104;
+static_assert(128 * kRegsMma + 256 * kRegsSoft + 128 * kRegsConv <= kThreads * kRegsLaunch, "register split");
+
+// ------------------------------------------------------------- the units --
+// Rows [rho0, rho1) of sequence b (row = token * G + head of the group) and
+// the position tiles that some row sees: those of the first positions that
+// stay visible, then the window's.
+struct Unit {
+    int64_t t0;                       // q row of the sequence's first token
+    int n, count, rho0, rho1, pmin, pmax, first_tile, sink_tiles, tiles;
+};
+template <int ROWS, int KT>
+__device__ __forceinline__ Unit unit_of(const PagedView &pv, const PrefillArgs &a, int b, int mb) {
+    Unit u;
+    const int64_t o0 = max((int64_t)0, min(a.T, a.q_off[b])), o1 = max(o0, min(a.T, a.q_off[b + 1]));
+    u.t0 = o0;
+    u.count = (int)(o1 - o0);
+    u.n = pv.length(b);
+    u.rho0 = mb * ROWS;
+    u.rho1 = min(u.rho0 + ROWS, u.count * a.G);
+    const int p0 = u.n - u.count;
+    u.pmin = p0 + u.rho0 / a.G;
+    u.pmax = p0 + (u.rho1 - 1) / a.G;
+    if (u.pmax < 0) {                 // no row sees anything: one tile, all masked
+        u.first_tile = u.sink_tiles = 0;
+        u.tiles = 1;
+        return u;
     }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float r = buf[0];
-    for (int i = 1; i < kT / 32; ++i) r = is_max ? fmaxf(r, buf[i]) : r + buf[i];
-    return r;
+    u.first_tile = pv.window_begin(max(u.pmin, 0)) / KT;
+    u.sink_tiles = min((min(pv.sinks, u.pmax + 1) + KT - 1) / KT, u.first_tile);
+    u.tiles = u.sink_tiles + u.pmax / KT - u.first_tile + 1;
+    return u;
+}
+template <int KT>
+__device__ __forceinline__ int tile_pos(const Unit &u, int t) {
+    return (t < u.sink_tiles ? t : u.first_tile + t - u.sink_tiles) * KT;
+}
+// every row sees every position of the tile at j0 (as far as the pages are there)
+template <int KT>
+__device__ __forceinline__ bool tile_full(const PagedView &pv, const Unit &u, int j0) {
+    return u.pmin >= 0 && j0 + KT - 1 <= u.pmin && (j0 >= pv.window_begin(u.pmax) || j0 + KT <= pv.sinks);
 }
 
-// One CTA per (token, query head): 128 positions at a time, a thread's
-// position each for the logits, a thread's two head elements each for P V.
-template <int FMT>
-__global__ void __launch_bounds__(kT)
-k_paged_attn_rows(PagedView pv, const __nv_bfloat16 *__restrict__ q, int64_t ld_q, const int64_t *__restrict__ q_off,
-                  int64_t B, int64_t T, int Hq, float scale, __nv_bfloat16 *__restrict__ out,
-                  float *__restrict__ lse) {
-    __shared__ float qs[kMaxDh], ps[kT], buf[kT / 32];
-    __shared__ int ss[kT];
-    const int64_t t = blockIdx.x / Hq;
-    const int hq = (int)(blockIdx.x % Hq), h = hq / (Hq / pv.H), Dh = pv.Dh, tid = threadIdx.x;
-    int64_t b = t;
-    int p;
-    if (q_off) {
-        int64_t lo = 0, hi = B - 1;
+constexpr int kPlanThreads = 1024;
+__device__ int64_t plan_scan(int64_t v, int64_t *buf, int64_t *total) {   // exclusive, block-wide
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) buf[warp] = x;
+    __syncthreads();
+    int64_t w = buf[lane], s = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += y;
+    }
+    *total = __shfl_sync(0xFFFFFFFFu, s, 31);
+    return __shfl_sync(0xFFFFFFFFu, s - w, warp) + x - v;
+}
+
+// One CTA: the row blocks of every sequence, their tiles, and where each CTA of
+// the attention kernel starts.
+template <int ROWS, int KT>
+__global__ void __launch_bounds__(kPlanThreads)
+k_prefill_plan(const PagedView pv, const PrefillArgs a) {
+    __shared__ int64_t buf[32];
+    pdl_wait();
+    pdl_trigger();
+    int64_t base = 0, all;
+    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+        const int b = b0 + threadIdx.x;
+        int64_t blocks = 0;
+        if (b < a.B) {
+            const int64_t o0 = max((int64_t)0, min(a.T, a.q_off[b])), o1 = max(o0, min(a.T, a.q_off[b + 1]));
+            blocks = ((o1 - o0) * a.G + ROWS - 1) / ROWS;
+        }
+        const int64_t pre = base + plan_scan(blocks, buf, &all);
+        if (b < a.B) a.first_block[b] = pre;
+        base += all;
+    }
+    const int64_t nb = min(base, a.max_blocks);   // more only if q_offsets decrease somewhere
+    __syncthreads();                  // first_block is read by the whole CTA
+    auto tiles_at = [&](int64_t i, int2 *who) -> int64_t {
+        if (i >= nb) return 0;
+        int lo = 0, hi = a.B - 1;     // the last sequence whose blocks begin at or before i
         while (lo < hi) {
-            const int64_t mid = (lo + hi + 1) / 2;
-            if (q_off[mid] <= t) lo = mid; else hi = mid - 1;
+            const int mid = (lo + hi + 1) / 2;
+            if (a.first_block[mid] <= i) lo = mid; else hi = mid - 1;
         }
-        b = lo;
-        const int64_t o0 = max((int64_t)0, min(T, q_off[b])), o1 = max((int64_t)0, min(T, q_off[b + 1]));
-        if (t < o0 || t >= o1) return;
-        p = (int)max((int64_t)-1, pv.length(b) - (o1 - o0) + (t - o0));
-    } else {
-        p = pv.length(b) - 1;
+        *who = make_int2(lo, (int)(i - a.first_block[lo]));
+        return (int64_t)unit_of<ROWS, KT>(pv, a, lo, who->y).tiles * pv.H;
+    };
+    int64_t sum = 0, total;
+    int2 who = make_int2(0, 0);
+    int64_t mine = 0;
+    for (int64_t i = threadIdx.x; i < nb; i += kPlanThreads) sum += mine = tiles_at(i, &who);
+    plan_scan(sum, buf, &total);
+    if (threadIdx.x == 0) {
+        a.hdr[0] = total;
+        a.hdr[1] = nb;
     }
-    for (int d = tid; d < Dh; d += kT) qs[d] = __bfloat162float(q[t * ld_q + (int64_t)hq * Dh + d]);
-    const int w0 = pv.window_begin(p), sinks = min(pv.sinks, w0);
-    const int vis = p + 1 - w0 + sinks;   // the sinks, then the window
-    float m = -INFINITY, l = 0.f, acc[2] = {0.f, 0.f};
-    bool any = false;
-    for (int i0 = 0; i0 < vis; i0 += kT) {
-        const int i = i0 + tid, j = i < sinks ? i : w0 + i - sinks;
-        const int s = i < vis ? pv.slot(b, j) : -1;
-        __syncthreads();
-        float z = -INFINITY;
-        if (s >= 0) {
-            const uint8_t *k = pv.kc + ((int64_t)s * pv.H + h) * Dh;
-            float a = 0.f;
-            for (int d = 0; d < Dh; ++d) a = fmaf(qs[d], fp8_to_float<FMT>(k[d]), a);
-            z = a * (pv.ks[(int64_t)s * pv.H + h] * scale);
-        }
-        any |= __syncthreads_or(s >= 0) != 0;
-        const float mn = fmaxf(m, block_reduce(z, true, buf));
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        const float w = s >= 0 ? expf(z - ref) : 0.f;
-        const float alpha = m == -INFINITY ? 0.f : expf(m - ref);
-        l = l * alpha + block_reduce(w, false, buf);
-        m = mn;
-        ss[tid] = s;
-        ps[tid] = s >= 0 ? w * pv.vs[(int64_t)s * pv.H + h] : 0.f;
-        __syncthreads();
-        acc[0] *= alpha;
-        acc[1] *= alpha;
-        for (int i1 = 0; i1 < kT; ++i1) {
-            const int si = ss[i1];
-            if (si < 0) continue;
-            const uint8_t *v = pv.vc + ((int64_t)si * pv.H + h) * Dh;
-            for (int e = 0; e < 2; ++e)
-                if (tid + e * kT < Dh) acc[e] = fmaf(ps[i1], fp8_to_float<FMT>(v[tid + e * kT]), acc[e]);
+    const int64_t n = min((int64_t)a.ctas, total);
+    base = 0;
+    for (int64_t i0 = 0; i0 < nb; i0 += kPlanThreads) {
+        const int64_t i = i0 + threadIdx.x;
+        if (nb > kPlanThreads || i >= nb) mine = tiles_at(i, &who);
+        const int64_t pre = base + plan_scan(mine, buf, &all);
+        base += all;
+        if (i < nb) {
+            a.block[i] = who;
+            // the CTAs whose first tile, total * c / n, lies here
+            for (int64_t c = (pre * n + total - 1) / total; c < n && total * c / n < pre + mine; ++c)
+                a.start[c] = make_longlong2(i, pre);
         }
     }
-    const int64_t row = t * Hq + hq;
-    for (int e = 0; e < 2; ++e)
-        if (tid + e * kT < Dh) out[row * Dh + tid + e * kT] = __float2bfloat16(any ? acc[e] / l : 0.f);
-    if (lse && tid == 0) lse[row] = any ? m + logf(l) : -INFINITY;
+}
+
+// --------------------------------------------------------------- PTX glue --
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag, uint32_t code) {
+    if (*abort_flag) return false;    // after a wait that ran out nobody waits again
+    return wait_bar(bar, parity, abort_flag, code);
+}
+__device__ __forceinline__ void arrive_release(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// 32 lanes x 16 columns from registers; tmem_st_wait() before they are read
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// waits for the loads in flight; the registers of this array cannot be read above it
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t pack_ff(float lo, float hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 0 at -inf and below 2^-126
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 .. 127
+template <int FMT>
+__device__ __forceinline__ void to_f16x4(uint32_t c, uint32_t &lo, uint32_t &hi) {   // four codes, exact
+    if (FMT == FP8_E4M3)
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(c));
+    else
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e5m2x2 %0, l;\n\tcvt.rn.f16x2.e5m2x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(c));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// bytes of four codes that are NaN or (E5M2) infinite: 0x80 in each such byte
+template <int FMT>
+__device__ __forceinline__ uint32_t nonfinite4(uint32_t c) {
+    return ((c & 0x7F7F7F7Fu) + (FMT == FP8_E4M3 ? 0x01010101u : 0x04040404u)) & 0x80808080u;
+}
+__device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// MN-major operand (V: a row per position, 64 head elements of 128 bytes per
+// swizzled block): 8 positions 1 KiB apart, blocks `block` bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr, uint32_t block) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(block >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+// kind::f16: fp32 sums, A and B fp16
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn) {
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// bits below x of a 32-bit word
+__device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u; }
+
+// ----------------------------------------------------------------- kernel --
+template <int FMT, int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+k_prefill(const PagedView pv, const PrefillArgs a) {
+    using P = Pre<DH>;
+    constexpr int MT = P::MT, KT = P::KT, ROWS = P::ROWS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint32_t s_tmem, s_abort, s_poison[8];
+    volatile uint32_t *abort_flag = &s_abort;
+    const uint32_t sb = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
+    const uint32_t bar0 = sb + P::OFF_BAR;
+    auto kfull = [&](int i) { return bar0 + 8 * i; };
+    auto kempty = [&](int i) { return bar0 + 8 * (2 + i); };
+    auto vfull = [&](int i) { return bar0 + 8 * (4 + i); };
+    auto vempty = [&](int i) { return bar0 + 8 * (6 + i); };
+    auto qfull = [&](int i) { return bar0 + 8 * (8 + i); };
+    auto sfull = [&](int i) { return bar0 + 8 * (8 + MT + i); };
+    auto pfull = [&](int i) { return bar0 + 8 * (8 + 2 * MT + i); };
+    auto pvdone = [&](int i) { return bar0 + 8 * (8 + 3 * MT + i); };
+    const uint32_t drain = bar0 + 8 * (8 + 4 * MT);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(kfull(i), 128);
+            mbar_init(vfull(i), 128);
+            mbar_init(kempty(i), 1);
+            mbar_init(vempty(i), 1);
+        }
+        for (int i = 0; i < MT; ++i) {
+            mbar_init(qfull(i), 128);
+            mbar_init(pfull(i), 128);
+            mbar_init(sfull(i), 1);
+            mbar_init(pvdone(i), 1);
+        }
+        mbar_init(drain, 1);
+        s_abort = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    pdl_wait();
+
+    // this CTA's run of tiles
+    const int64_t total = a.hdr[0], ncta = min((int64_t)a.ctas, total);
+    const bool active = (int64_t)blockIdx.x < ncta;
+    int64_t at = 0, end = 0;
+    int bi = 0, h = 0, tile = 0;      // row block, head, tile in the unit
+    int2 who = make_int2(0, 0);
+    Unit u = {};
+    if (active) {
+        at = total * blockIdx.x / ncta;
+        end = total * (blockIdx.x + 1) / ncta;
+        const longlong2 s = a.start[blockIdx.x];
+        bi = (int)s.x;
+        who = a.block[bi];
+        u = unit_of<ROWS, KT>(pv, a, who.x, who.y);
+        h = (int)((at - s.y) / u.tiles);
+        tile = (int)((at - s.y) % u.tiles);
+    }
+    // to the next unit, after `done` tiles of this one
+    auto advance = [&](int done) {
+        at += done;
+        tile = 0;
+        if (at < end && ++h == pv.H) {
+            h = 0;
+            who = a.block[++bi];
+            u = unit_of<ROWS, KT>(pv, a, who.x, who.y);
+        }
+    };
+    auto run_length = [&] { return (int)min((int64_t)(u.tiles - tile), end - at); };
+
+    if (wg == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------------ MMAs --
+            constexpr uint32_t id_s = idesc_f16(128, KT, false), id_o = idesc_f16(128, DH, true);
+            uint32_t kc = 0, seg = 0, pc[2] = {0, 0};   // tiles so far; runs; P tiles so far
+            uint32_t qc[2] = {0, 0};
+            bool ok = true;
+            auto issue_s = [&](int i, uint32_t buf) {
+                const uint32_t qa = sb + i * P::QB, ka = sb + P::OFF_K + buf * P::KVB;
+#pragma unroll
+                for (int blk = 0; blk < DH / 64; ++blk) {
+                    const uint64_t qd = sdesc_k_sw128(qa + blk * 128 * 128), kd = sdesc_k_sw128(ka + blk * KT * 128);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        mma_ss(tmem + i * P::S_COL, qd + 2 * s, kd + 2 * s, id_s, (blk | s) ? 1u : 0u);
+                }
+                tc_commit(sfull(i));
+            };
+            while (ok && at < end) {
+                const int len = run_length(), tiles_m = u.rho1 - u.rho0 > 128 ? MT : 1;
+                for (int i = 0; ok && i < tiles_m; ++i) ok = wait_for(qfull(i), qc[i]++ & 1u, abort_flag, kErrMma);
+                ok = ok && wait_for(kfull(kc & 1), (kc >> 1) & 1u, abort_flag, kErrMma);
+                if (!ok) break;
+                tc_fence_after();
+                for (int i = 0; i < tiles_m; ++i) issue_s(i, kc & 1);
+                tc_commit(kempty(kc & 1));
+                for (int k = 0; ok && k < len; ++k, ++kc) {
+                    ok = wait_for(vfull(kc & 1), (kc >> 1) & 1u, abort_flag, kErrMma);
+                    for (int i = 0; ok && i < tiles_m; ++i) {
+                        ok = wait_for(pfull(i), pc[i]++ & 1u, abort_flag, kErrMma);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vd = sdesc_mn(sb + P::OFF_V + (kc & 1) * P::KVB, KT * 128);
+#pragma unroll
+                        for (int s = 0; s < KT / 16; ++s)
+                            mma_ts(tmem + P::O_COL + i * DH, tmem + i * P::S_COL + 8 * s, vd + 128 * s, id_o,
+                                   (k | s) ? 1u : 0u);
+                        tc_commit(pvdone(i));
+                        if (k + 1 < len) {
+                            if (i == 0) ok = wait_for(kfull((kc + 1) & 1), ((kc + 1) >> 1) & 1u, abort_flag, kErrMma);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue_s(i, (kc + 1) & 1);
+                        }
+                    }
+                    if (!ok) break;
+                    tc_commit(vempty(kc & 1));
+                    if (k + 1 < len) tc_commit(kempty((kc + 1) & 1));
+                }
+                advance(len);
+                ++seg;
+            }
+            tc_commit(drain);
+            wait_bar_drain(drain, 0u);
+        }
+        __syncwarp();
+    } else if (wg == 3) {
+        // ------------------------------------------- K and V converter ----
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
+        constexpr int CH = DH / 16, RPI = 32 / CH, ITS = KT / (4 * RPI);   // 16-code chunks of a row; rows per load
+        const int tid = threadIdx.x - 384, w = tid >> 5, c = lane % CH, r0 = w * RPI + lane / CH;
+        const int swap = (c >> 2) & 1;        // half the chunks are stored high half first: no bank conflicts
+        const bool c_live = 16 * c < pv.Dh;
+        const uint64_t row_bytes = (uint64_t)pv.H * pv.Dh;
+        uint32_t kc = 0, seg = 0;
+        int ex = -1000;                       // exponent of the largest V scale of the run so far
+        auto wg_sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        auto meta = [&](uint32_t k) { return smem + P::OFF_M + (k % P::META) * P::M_BYTES; };
+        // slots and scales of tile t (the k-th of this CTA) of unit u; head hh
+        auto look_up = [&](uint32_t k, int t, bool fresh) {
+            uint8_t *m = meta(k);
+            float dv = 0.0f;
+            if (tid < KT) {
+                const int j = tile_pos<KT>(u, t) + tid;
+                const int s = j < u.n && j <= u.pmax ? pv.slot(who.x, j) : -1;
+                float dk = 0.0f;
+                if (s >= 0) {
+                    dk = pv.ks[(int64_t)s * pv.H + h];
+                    dv = pv.vs[(int64_t)s * pv.H + h];
+                }
+                reinterpret_cast<float *>(m + P::M_DK)[tid] = dk;
+                reinterpret_cast<float *>(m + P::M_DV)[tid] = dv;
+                reinterpret_cast<int *>(m + P::M_SLOT)[tid] = s;
+                const uint32_t live = __ballot_sync(0xFFFFFFFFu, s >= 0);
+                const float d = fabsf(dv);
+                const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, d < INFINITY ? __float_as_uint(d) : 0u);
+                if (lane == 0) {
+                    reinterpret_cast<uint32_t *>(m + P::M_LIVE)[w] = live;
+                    reinterpret_cast<uint32_t *>(m + P::M_MAX)[w] = mx;
+                }
+            }
+            if (fresh && tid == 0) s_poison[seg & 7] = 0u;
+            wg_sync();
+            uint32_t mx = 0;
+#pragma unroll
+            for (int i = 0; i < KT / 32; ++i) mx = max(mx, reinterpret_cast<const uint32_t *>(m + P::M_MAX)[i]);
+            if (fresh) ex = -1000;
+            if (mx) ex = max(ex, max((int)(mx >> 23) - 127, -100));
+            if (tid == 0) *reinterpret_cast<int *>(m + P::M_EXP) = ex;
+        };
+        auto load = [&](uint4 (&v)[ITS], const uint8_t *codes, uint32_t k) {
+            const int *slot = reinterpret_cast<const int *>(meta(k) + P::M_SLOT);
+#pragma unroll
+            for (int i = 0; i < ITS; ++i) {
+                const int s = slot[i * 4 * RPI + r0];
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (s >= 0 && c_live)
+                    v[i] = *reinterpret_cast<const uint4 *>(codes + (uint64_t)(uint32_t)s * row_bytes + h * pv.Dh + 16 * c);
+            }
+        };
+        auto put = [&](uint32_t base, int row, const uint32_t (&x)[8]) {
+            const uint32_t at_row = base + (c >> 2) * (KT * 128) + row * 128, ch = (c & 3) * 2;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int hf = e ^ swap;
+                const uint32_t dst = at_row + (((ch + hf) ^ (row & 7)) << 4);
+                if (hf) st_shared16(dst, x[4], x[5], x[6], x[7]);
+                else st_shared16(dst, x[0], x[1], x[2], x[3]);
+            }
+        };
+        uint4 kv[ITS], vv[ITS];
+        if (at < end) {
+            look_up(0, tile, true);
+            load(kv, pv.kc, 0);
+            load(vv, pv.vc, 0);
+        }
+        while (at < end) {
+            const int len = run_length();
+            for (int k = 0; k < len; ++k, ++kc) {
+                const uint32_t buf = kc & 1, par = ((kc >> 1) & 1u) ^ 1u;
+                const int j0 = tile_pos<KT>(u, tile + k);
+                const bool full = tile_full<KT>(pv, u, j0);
+                const int my_ex = ex;
+                uint8_t *m = meta(kc);
+                // ---- K
+                wait_for(kempty(buf), par, abort_flag, kErrProducer);
+                const uint32_t kb = sb + P::OFF_K + buf * P::KVB;
+#pragma unroll
+                for (int i = 0; i < ITS; ++i) {
+                    uint32_t x[8];
+                    to_f16x4<FMT>(kv[i].x, x[0], x[1]);
+                    to_f16x4<FMT>(kv[i].y, x[2], x[3]);
+                    to_f16x4<FMT>(kv[i].z, x[4], x[5]);
+                    to_f16x4<FMT>(kv[i].w, x[6], x[7]);
+                    put(kb, i * 4 * RPI + r0, x);
+                }
+                fence_async();
+                arrive_release(kfull(buf));
+                // ---- the next tile's slots, and its K on the way while V is converted
+                bool more = k + 1 < len;
+                const uint32_t this_seg = seg;
+                if (more) {
+                    look_up(kc + 1, tile + k + 1, false);
+                } else if (at + len < end) {
+                    advance(len);
+                    ++seg;
+                    look_up(kc + 1, 0, true);
+                    more = true;
+                } else {
+                    at = end;
+                }
+                if (more) load(kv, pv.kc, kc + 1);
+                // ---- V, scaled
+                wait_for(vempty(buf), par, abort_flag, kErrProducer);
+                const uint32_t vb = sb + P::OFF_V + buf * P::KVB;
+                const float fp = my_ex > -1000 ? pow2i(max((FMT == FP8_E4M3 ? P::VC_E4M3 : P::VC_E5M2) - my_ex, -126)) : 0.0f;
+                const float *dv = reinterpret_cast<const float *>(m + P::M_DV);
+                uint32_t bad = 0;
+#pragma unroll
+                for (int i = 0; i < ITS; ++i) {
+                    const int row = i * 4 * RPI + r0;
+                    float f = dv[row] * fp;
+                    uint4 q = vv[i];
+                    if (!full) {              // what only some rows see must be finite
+                        const uint32_t nf = nonfinite4<FMT>(q.x) | nonfinite4<FMT>(q.y) | nonfinite4<FMT>(q.z) |
+                                            nonfinite4<FMT>(q.w);
+                        if (nf | !(fabsf(f) < INFINITY)) {
+                            bad = 1;
+                            auto clean = [](uint32_t x) {
+                                const uint32_t b = nonfinite4<FMT>(x);
+                                return x & ~((b >> 7) * 0xFFu);
+                            };
+                            q = make_uint4(clean(q.x), clean(q.y), clean(q.z), clean(q.w));
+                            if (!(fabsf(f) < INFINITY)) f = 0.0f;
+                        }
+                    }
+                    const uint32_t f2 = pack_f16x2(f, f);
+                    uint32_t x[8];
+                    to_f16x4<FMT>(q.x, x[0], x[1]);
+                    to_f16x4<FMT>(q.y, x[2], x[3]);
+                    to_f16x4<FMT>(q.z, x[4], x[5]);
+                    to_f16x4<FMT>(q.w, x[6], x[7]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = mul_f16x2(x[e], f2);
+                    put(vb, row, x);
+                }
+                if (bad) s_poison[this_seg & 7] = 1u;
+                fence_async();
+                arrive_release(vfull(buf));
+                if (more) load(vv, pv.vc, kc + 1);
+                if (k + 1 == len && more) {   // advanced already: the next run begins
+                    ++kc;
+                    break;
+                }
+            }
+        }
+    } else if (wg - 1 < MT) {
+        // --------------------------------------------- softmax, results ---
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        const int mi = wg - 1, row = threadIdx.x - 128 * wg;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lane_base + mi * P::S_COL, to = tmem + lane_base + P::O_COL + mi * DH;
+        uint32_t kc = 0, sc = 0, seg = 0;     // tiles of the CTA; S tiles of this row tile; runs
+        while (at < end) {
+            const int len = run_length();
+            const bool mine = mi == 0 || u.rho1 - u.rho0 > 128;
+            if (!mine) {
+                kc += len;
+                advance(len);
+                ++seg;
+                continue;
+            }
+            const int rho = u.rho0 + mi * 128 + row;
+            const bool valid = rho < u.rho1;
+            const int tok = rho / a.G, g = rho - tok * a.G;
+            const int p = valid ? u.n - u.count + tok : -1;
+            const int wb = p >= 0 ? pv.window_begin(p) : 0;
+            const int64_t orow = (u.t0 + tok) * (int64_t)pv.H * a.G + (int64_t)h * a.G + g;
+            // ---- Q: this thread's row as fp16, by a power of two
+            float cf;
+            {
+                const __nv_bfloat16 *qp = a.q + (u.t0 + tok) * a.ld_q + (int64_t)(h * a.G + g) * pv.Dh;
+                uint32_t mx = 0;
+#pragma unroll
+                for (int c = 0; c < DH / 8; ++c) {
+                    if (valid && 8 * c < pv.Dh) {
+                        uint32_t bad = 0;
+                        mx = amax_exact8(mx, *reinterpret_cast<const uint4 *>(qp + 8 * c), bad);
+                    }
+                }
+                const int e = max((int)(mx >> 7), 14) - 127;
+                const float up = a.scale < 0.0f ? -pow2i(14 - e) : pow2i(14 - e);   // the sign of the scale goes to Q
+                cf = fmaxf(fabsf(a.scale) * kLog2e * pow2i(e) * 0x1p-14f, 1e-37f);   // positive: -inf stays -inf
+                const uint32_t qa = sb + mi * P::QB + row * 128;
+#pragma unroll
+                for (int c = 0; c < DH / 8; ++c) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (valid && 8 * c < pv.Dh) v = *reinterpret_cast<const uint4 *>(qp + 8 * c);
+                    st_shared16(qa + (c >> 3) * (128 * 128) + (((c & 7) ^ (row & 7)) << 4),
+                                pack_f16x2(bf_lo(v.x) * up, bf_hi(v.x) * up), pack_f16x2(bf_lo(v.y) * up, bf_hi(v.y) * up),
+                                pack_f16x2(bf_lo(v.z) * up, bf_hi(v.z) * up), pack_f16x2(bf_lo(v.w) * up, bf_hi(v.w) * up));
+                }
+                fence_async();
+                arrive_release(qfull(mi));
+            }
+            float mr = kNoMax, l = 0.0f;
+            int ex = -1000;
+            for (int k = 0; k < len; ++k, ++kc, ++sc) {
+                const uint8_t *m = smem + P::OFF_M + (kc % P::META) * P::M_BYTES;
+                const int j0 = tile_pos<KT>(u, tile + k);
+                wait_for(sfull(mi), sc & 1u, abort_flag, kErrEpilogue);
+                tc_fence_after();
+                uint32_t x[KT];
+#pragma unroll
+                for (int i = 0; i < KT / 32; ++i) tmem_ld32_async(ts + 32 * i, x + 32 * i);
+                tmem_ld_wait(x);
+                // ---- times K's scales
+                const float4 *dk = reinterpret_cast<const float4 *>(m + P::M_DK);
+#pragma unroll
+                for (int i = 0; i < KT / 4; ++i) {
+                    const float4 d = dk[i];
+                    const uint64_t lo = mul_f32x2(pack_f32x2(x[4 * i], x[4 * i + 1]), pack_ff(d.x, d.y));
+                    const uint64_t hi = mul_f32x2(pack_f32x2(x[4 * i + 2], x[4 * i + 3]), pack_ff(d.z, d.w));
+                    x[4 * i] = (uint32_t)lo;
+                    x[4 * i + 1] = (uint32_t)(lo >> 32);
+                    x[4 * i + 2] = (uint32_t)hi;
+                    x[4 * i + 3] = (uint32_t)(hi >> 32);
+                }
+                // ---- what the row does not see
+                const uint32_t *live = reinterpret_cast<const uint32_t *>(m + P::M_LIVE);
+                uint32_t all = 0xFFFFFFFFu;
+#pragma unroll
+                for (int i = 0; i < KT / 32; ++i) all &= live[i];
+                if (all != 0xFFFFFFFFu || !tile_full<KT>(pv, u, j0)) {
+#pragma unroll
+                    for (int i = 0; i < KT / 32; ++i) {
+                        const int c0 = j0 + 32 * i;
+                        const uint32_t see = below(p + 1 - c0) & (~below(wb - c0) | below(pv.sinks - c0)) & live[i];
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!((see >> c) & 1u)) x[32 * i + c] = 0xFF800000u;   // -inf
+                    }
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < KT; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cf;
+                // ---- the reference, and O against it and V's exponent
+                const int ex_new = *reinterpret_cast<const int *>(m + P::M_EXP);
+                const bool up = top > mr + kAbove;
+                if (__any_sync(0xFFFFFFFFu, up) || ex_new != ex) {
+                    float al = 1.0f;
+                    if (up) {
+                        al = exp2_fast(mr - (top - kBelow));
+                        mr = top - kBelow;
+                        l *= al;
+                    }
+                    if (k > 0) {
+                        if (ex_new != ex) al *= ex > -1000 && ex - ex_new >= -126 ? pow2i(ex - ex_new) : 0.0f;
+                        wait_for(pvdone(mi), (sc - 1) & 1u, abort_flag, kErrEpilogue);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < DH; c += 16) {
+                            uint32_t o[16];
+                            asm volatile(
+                                "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                                "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
+                                  "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]),
+                                  "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+                                : "r"(to + c));
+                            tmem_ld_wait(o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                            tmem_st16(to + c, o);
+                        }
+                        tmem_st_wait();
+                    }
+                    ex = ex_new;
+                }
+                // ---- P = exp2(x cf - mr), fp16, over S's columns
+                const uint64_t cf2 = pack_ff(cf, cf), mr2 = pack_ff(-mr, -mr);
+                uint64_t sum = 0ull;
+#pragma unroll
+                for (int i = 0; i < KT / 32; ++i) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const uint64_t e = fma_f32x2(pack_f32x2(x[32 * i + 2 * c], x[32 * i + 2 * c + 1]), cf2, mr2);
+                        float e0, e1;
+                        unpack_f32x2(e, e0, e1);
+                        e0 = exp2_fast(e0);
+                        e1 = exp2_fast(e1);
+                        sum = add_f32x2(sum, pack_ff(e0, e1));
+                        pk[c] = pack_f16x2(e0, e1);
+                    }
+                    tmem_st16(ts + 16 * i, pk);
+                }
+                float s0, s1;
+                unpack_f32x2(sum, s0, s1);
+                l += s0 + s1;
+                tmem_st_wait();
+                tc_fence_before();
+                arrive_release(pfull(mi));
+            }
+            // ---- this run's result
+            wait_for(pvdone(mi), (sc - 1) & 1u, abort_flag, kErrEpilogue);
+            tc_fence_after();
+            const bool whole = tile == 0 && len == u.tiles;
+            const int64_t unit = (int64_t)bi * pv.H + h;
+            if (tile == 0 && threadIdx.x == 128) {
+                // the CTA that holds tile x is the largest c with total * c / ncta <= x
+                const int64_t last = whole ? blockIdx.x : ((at + u.tiles - 1) * ncta + ncta - 1) / total;
+                a.span[unit] = make_int2(blockIdx.x, (int)last);
+            }
+            constexpr int vc = FMT == FP8_E4M3 ? P::VC_E4M3 : P::VC_E5M2;
+            const float fo = ex > -1000 ? pow2i(min(ex - vc, 127)) : 0.0f;
+            const float r = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+            float *part = a.part + ((int64_t)blockIdx.x * 2 + (tile == 0 ? 1 : 0)) * ((int64_t)ROWS * (DH + 2));
+            const bool poison = s_poison[seg & 7] != 0u;
+#pragma unroll 1
+            for (int c = 0; c < DH; c += 32) {
+                uint32_t o[32];
+                tmem_ld32_async(to + c, o);
+                tmem_ld_wait(o);
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * fo;
+                if (poison) {
+                    // values that were taken out of V: back into the rows that see them
+#pragma unroll 1
+                    for (int k = 0; k < len; ++k) {
+                        const int j0 = tile_pos<KT>(u, tile + k);
+                        if (tile_full<KT>(pv, u, j0)) continue;
+#pragma unroll 1
+                        for (int j = j0; j < j0 + KT; ++j) {
+                            if (j > p || !(j >= wb || j < pv.sinks)) continue;
+                            const int s = pv.slot(who.x, j);
+                            if (s < 0) continue;
+                            const float d = pv.vs[(int64_t)s * pv.H + h];
+                            const uint8_t *codes = pv.vc + (uint64_t)(uint32_t)s * (uint64_t)(pv.H * pv.Dh) + h * pv.Dh + c;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i < pv.Dh) {
+                                    const float w = fp8x2_to_float2<FMT>((uint16_t)codes[i]).x * d;
+                                    if (!(fabsf(w) < INFINITY)) v[i] += w;
+                                }
+                        }
+                    }
+                }
+                if (!valid || c >= pv.Dh) continue;
+                if (whole) {
+                    __nv_bfloat16 *op = a.out + orow * pv.Dh + c;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        if (c + i < pv.Dh) {
+                            uint4 w;
+                            w.x = pack_bf16x2(v[i] * r, v[i + 1] * r);
+                            w.y = pack_bf16x2(v[i + 2] * r, v[i + 3] * r);
+                            w.z = pack_bf16x2(v[i + 4] * r, v[i + 5] * r);
+                            w.w = pack_bf16x2(v[i + 6] * r, v[i + 7] * r);
+                            *reinterpret_cast<uint4 *>(op + i) = w;
+                        }
+                } else {
+                    float *pp = part + (int64_t)(mi * 128 + row) * DH + c;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4 *>(pp + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                }
+            }
+            tc_fence_before();
+            if (valid) {
+                if (whole) {
+                    if (a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : (mr + log2f(l)) * kLn2;
+                } else {
+                    *reinterpret_cast<float2 *>(part + (int64_t)ROWS * DH + 2 * (mi * 128 + row)) = make_float2(mr, l);
+                }
+            }
+            advance(len);
+            ++seg;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    }
+}
+
+// Joins the parts of the units that more than one CTA worked on: a warp per
+// row, a lane per DH / 32 elements, the CTAs in order.
+template <int DH>
+__global__ void __launch_bounds__(256)
+k_prefill_join(const PagedView pv, const PrefillArgs a) {
+    using P = Pre<DH>;
+    constexpr int E = DH / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
+    const int64_t bi = blockIdx.x / pv.H;
+    const int h = (int)(blockIdx.x % pv.H);
+    if (bi >= a.hdr[1]) return;
+    const int2 span = a.span[blockIdx.x];
+    if (span.x == span.y) return;
+    const int2 who = a.block[bi];
+    const Unit u = unit_of<P::ROWS, P::KT>(pv, a, who.x, who.y);
+    const int64_t stride = (int64_t)P::ROWS * (DH + 2);
+    for (int row = blockIdx.y * 8 + warp; row < u.rho1 - u.rho0; row += gridDim.y * 8) {
+        const int rho = u.rho0 + row, tok = rho / a.G, g = rho - tok * a.G;
+        const int64_t orow = (u.t0 + tok) * (int64_t)pv.H * a.G + (int64_t)h * a.G + g;
+        float mx = kNoMax, sum = 0.0f, acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+        for (int c = span.x; c <= span.y; ++c) {
+            const float *p = a.part + (2 * (int64_t)c + (c == span.x ? 1 : 0)) * stride;
+            const float2 v = *reinterpret_cast<const float2 *>(p + (int64_t)P::ROWS * DH + 2 * row);
+            const float nm = fmaxf(mx, v.x), al = exp2_fast(mx - nm), be = exp2_fast(v.x - nm);
+            mx = nm;
+            sum = fmaf(sum, al, v.y * be);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] = fmaf(acc[e], al, p[(int64_t)row * DH + lane * E + e] * be);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (lane * E + e < pv.Dh)
+                a.out[orow * pv.Dh + lane * E + e] = __float2bfloat16(sum == 0.0f ? 0.0f : acc[e] / sum);
+        if (lane == 0 && a.lse) a.lse[orow] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+    }
 }
 
 }  // namespace
 
 using namespace fp8q_host;
 
+namespace {
+
+struct PrefillPlan {
+    int DH, ctas;
+    int64_t units;            // at most, over all heads
+    size_t part, span, hdr, first, block, start, total;
+};
+
+PrefillPlan prefill_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t Dh, int sms) {
+    PrefillPlan p;
+    const int64_t G = Hq / H;
+    p.DH = Dh <= 64 ? 64 : Dh <= 128 ? 128 : 256;
+    p.ctas = sms;
+    const int64_t rows = p.DH <= 128 ? 256 : 128, blocks = T * G / rows + std::min(B, T);
+    p.units = blocks * H;
+    size_t at = 0;
+    auto take = [&at](size_t n) {
+        const size_t was = at;
+        at += (n + 255) & ~(size_t)255;
+        return was;
+    };
+    p.part = take((size_t)p.ctas * 2 * rows * (p.DH + 2) * 4);
+    p.span = take((size_t)p.units * 8);
+    p.hdr = take(16);
+    p.first = take((size_t)(B + 1) * 8);
+    p.block = take((size_t)blocks * 8);
+    p.start = take((size_t)p.ctas * 16);
+    p.total = at;
+    return p;
+}
+
+template <int FMT, int DH>
+cudaError_t launch_prefill(const PagedView &pv, const PrefillArgs &a, const PrefillPlan &p, cudaStream_t s) {
+    using P = Pre<DH>;
+    // shared memory and the register split are checked once per device
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, k_prefill<FMT, DH>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;   // setmaxnreg needs exactly these
+        e = cudaFuncSetAttribute(k_prefill<FMT, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::SMEM);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    e = pdl_launch(k_prefill_plan<P::ROWS, P::KT>, dim3(1), dim3(kPlanThreads), 0, s, pv, a);
+    if (e != cudaSuccess) return e;
+    e = pdl_launch(k_prefill<FMT, DH>, dim3(p.ctas), dim3(kThreads), P::SMEM, s, pv, a);
+    if (e != cudaSuccess) return e;
+    const unsigned slices = (unsigned)std::max<int64_t>(1, std::min<int64_t>(16, 2048 / p.units));
+    return pdl_launch(k_prefill_join<DH>, dim3((unsigned)p.units, slices), dim3(256), 0, s, pv, a);
+}
+
+}  // namespace
+
 fp8_status fp8q_host::prefill_workspace(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t Dh, size_t *bytes) {
-    *bytes = 0;
+    int sms;
+    const fp8_status st = check_device(&sms);
+    if (st != FP8_OK) return st;
+    *bytes = prefill_plan(T, B, Hq, H, Dh, sms).total;
     return FP8_OK;
 }
 
@@ -121,14 +972,45 @@ extern "C" fp8_status fp8_paged_attention_prefill(
     int sms;
     st = check_device(&sms);
     if (st != FP8_OK) return st;
+    const PrefillPlan p = prefill_plan(T, B, Hq, H, Dh, sms);
+    if (!workspace || workspace_bytes < p.total) return FP8_ERR_INVALID_ARG;
     const PagedView pv = make_paged_view(k_cache, k_scale, v_cache, v_scale, H, Dh, block_size, num_blocks,
                                          block_table, seq_lens, max_blocks, window, sinks);
+    uint8_t *ws = (uint8_t *)workspace;
+    PrefillArgs a = {};
+    a.q = (const __nv_bfloat16 *)q_bf16;
+    a.ld_q = ld_q;
+    a.q_off = q_offsets;
+    a.T = T;
+    a.B = (int)B;
+    a.G = (int)(Hq / H);
+    a.ctas = p.ctas;
+    a.max_blocks = p.units / H;
+    a.scale = softmax_scale;
+    a.out = (__nv_bfloat16 *)out_bf16;
+    a.lse = lse;
+    a.part = (float *)(ws + p.part);
+    a.span = (int2 *)(ws + p.span);
+    a.hdr = (int64_t *)(ws + p.hdr);
+    a.first_block = (int64_t *)(ws + p.first);
+    a.block = (int2 *)(ws + p.block);
+    a.start = (longlong2 *)(ws + p.start);
     cudaStream_t s = as_stream(stream);
-    auto run = [&](auto rows) {
-        rows<<<dim3((unsigned)(T * Hq)), kT, 0, s>>>(pv, (const __nv_bfloat16 *)q_bf16, ld_q, q_offsets, B, T,
-                                                     (int)Hq, softmax_scale, (__nv_bfloat16 *)out_bf16, lse);
-    };
-    if (fmt == FP8_E4M3) run(k_paged_attn_rows<FP8_E4M3>);
-    else run(k_paged_attn_rows<FP8_E5M2>);
-    return cudaPeekAtLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+    cudaError_t e;
+    if (p.DH == 64) e = fmt == FP8_E4M3 ? launch_prefill<FP8_E4M3, 64>(pv, a, p, s) : launch_prefill<FP8_E5M2, 64>(pv, a, p, s);
+    else if (p.DH == 128) e = fmt == FP8_E4M3 ? launch_prefill<FP8_E4M3, 128>(pv, a, p, s) : launch_prefill<FP8_E5M2, 128>(pv, a, p, s);
+    else e = fmt == FP8_E4M3 ? launch_prefill<FP8_E4M3, 256>(pv, a, p, s) : launch_prefill<FP8_E5M2, 256>(pv, a, p, s);
+    return e == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+}
+
+// This file's device error word (fp8_device_error reads it with the others').
+fp8_status fp8q_prefill_device_error(uint32_t *out, int clear) {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_gemm_error, sizeof(v)) != cudaSuccess) return FP8_ERR_CUDA;
+    *out = v;
+    if (clear) {
+        const unsigned int z = 0;
+        if (cudaMemcpyToSymbol(g_gemm_error, &z, sizeof(z)) != cudaSuccess) return FP8_ERR_CUDA;
+    }
+    return FP8_OK;
 }

@@ -39,9 +39,10 @@ class Cache:
         self.v = vals[v.cache.cpu().reshape(-1, k.H, k.Dh).long()] * v.scale_inv.cpu().reshape(-1, k.H, 1).double()
 
 
-def attend(cache, table_row, n, p, q, h, scale, window=0, sinks=0):
+def attend(cache, table_row, n, p, q, h, scale, window=0, sinks=0, scaled_v=False):
     """q [G, Dh] at position p of a sequence of n tokens, KV head h -> dict of out [G, Dh], lse [G], positions,
-    weights [G, visible], and the bounds: ez [G] on a logit, tol [G, Dh] on out."""
+    weights [G, visible], and the bounds: ez [G] on a logit, tol [G, Dh] on out (scaled_v: of the kernel for several
+    tokens, whose fp16 V holds the rows' scales)."""
     G, Dh = q.shape
     js, ss = [], []
     for j in range(0, min(n, p + 1)):
@@ -71,7 +72,18 @@ def attend(cache, table_row, n, p, q, h, scale, window=0, sinks=0):
     # with f max(d) >= 2^8, and p_j = exp(z_j - r) for a reference r that is at most the largest logit, so that
     # l = sum p >= 1.  Rounding below 2^-14 is off by at most 2^-25 for each j, which reaches the result divided by f l:
     # 2^-25 sum |code_j| / (f l) <= 2^-33 max(d) sum |code_j|.
-    tol = tol + 2.0 ** -33 * cache.vscale[ss, h].double().abs().max() * cache.vcode[ss, h].abs().sum(0)
+    dmax, codes = cache.vscale[ss, h].double().abs().max(), cache.vcode[ss, h].abs().sum(0)
+    if scaled_v:
+        # fp16 V = code_j d_j f: the factor d_j f and the product are rounded once each (2^-11 more, twice), and below
+        # 2^-14 the product is off by at most 2^-25, that is 2^-25 / f in the result, a weighted mean.  f is a power
+        # of two with f max(d) >= 2^6 (E4M3) or 2^-1 (E5M2), the maximum over every live position of the sequence.
+        # The weights reach at least 2^7 (l >= 2^7), so that theirs loses at most 2^-32 max(d) sum |code_j|.
+        live = [x for x in (slot_of(table_row, j, cache.bs, cache.nb) for j in range(n)) if x is not None]
+        dall = cache.vscale[live, h].double().abs().max()
+        tol = tol + (1 + 2.0 ** -7) * 2.0 ** -10 * (w @ v.abs()) + 2.0 ** (-31 if cache.fmt == 0 else -24) * dall
+        tol = tol + 2.0 ** -32 * dmax * codes
+    else:
+        tol = tol + 2.0 ** -33 * dmax * codes
     return dict(out=out, lse=lse, pos=js, w=w, ez=ez, tol=tol + 1e-30)
 
 

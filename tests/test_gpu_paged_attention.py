@@ -35,7 +35,8 @@ def make_caches(lens, H, Dh, bs, fmt, seed, spare=2, stale=True):
     return caches[0], caches[1], table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
 
 
-def check_rows(out, lse, q, k, v, table, lens, rows, scale, window, sinks, mass=None, mass0=None, decay=0.0):
+def check_rows(out, lse, q, k, v, table, lens, rows, scale, window, sinks, mass=None, mass0=None, decay=0.0,
+               scaled_v=False):
     """rows: (t, b, p) of every query row; out / lse [T, Hq, ...]."""
     host = ref.Cache(k, v)
     H, G = k.H, q.shape[1] // k.H
@@ -45,7 +46,7 @@ def check_rows(out, lse, q, k, v, table, lens, rows, scale, window, sinks, mass=
         n = min(max(int(lens[b]), 0), cap)
         for h in range(H):
             sl = slice(h * G, (h + 1) * G)
-            r = ref.attend(host, th[b].tolist(), n, p, qh[t, sl], h, scale, window, sinks)
+            r = ref.attend(host, th[b].tolist(), n, p, qh[t, sl], h, scale, window, sinks, scaled_v)
             err = (oh[t, sl] - r["out"]).abs()
             assert torch.all(err <= r["tol"]), (t, h, float((err / r["tol"]).max()))
             if not r["pos"]:
@@ -137,7 +138,7 @@ def test_prefill(case):
     q = inputs.normal_bf16((T, H * G, Dh), 1.0, seed=6).to(DEV)
     out, lse = fp8q.paged_attention_prefill(q, off.to(DEV), k, v, table, ln, window, sinks)
     rows = [(int(off[b]) + i, b, n - m + i) for b, (n, m) in enumerate(seqs) for i in range(m)]
-    check_rows(out, lse, q, k, v, table, lens, rows, Dh ** -0.5, window, sinks)
+    check_rows(out, lse, q, k, v, table, lens, rows, Dh ** -0.5, window, sinks, scaled_v=True)
 
 
 def test_prefill_rows_of_no_sequence_are_left_alone_and_short_sequences_see_nothing():
@@ -155,7 +156,7 @@ def test_prefill_rows_of_no_sequence_are_left_alone_and_short_sequences_see_noth
     for t in (0, 1, 2, 14, 15, 19):
         assert torch.all(out[t] == 7.0) and torch.all(lse[t] == 5.0)
     rows = [(3 + i, 0, -2 + i) for i in range(6)] + [(9 + i, 1, 4 + i) for i in range(5)]
-    check_rows(out, lse, q, k, v, table, lens, rows, 0.125, 0, 0)
+    check_rows(out, lse, q, k, v, table, lens, rows, 0.125, 0, 0, scaled_v=True)
 
 
 def test_prefill_of_one_token_agrees_with_decode():
@@ -166,7 +167,7 @@ def test_prefill_of_one_token_agrees_with_decode():
     b, lb = fp8q.paged_attention_prefill(q, torch.tensor([0, 1, 2], device=DEV), k, v, table, ln)
     rows = [(i, i, n - 1) for i, n in enumerate(lens)]
     check_rows(a, la, q, k, v, table, lens, rows, 128 ** -0.5, 0, 0)
-    check_rows(b, lb, q, k, v, table, lens, rows, 128 ** -0.5, 0, 0)
+    check_rows(b, lb, q, k, v, table, lens, rows, 128 ** -0.5, 0, 0, scaled_v=True)
 
 
 @pytest.mark.parametrize("kind", ["decode", "prefill"])
@@ -191,7 +192,8 @@ def test_bad_pages_are_not_visible_and_lengths_are_clamped(kind):
     else:
         out, lse = fp8q.paged_attention_prefill(q, torch.tensor([0, 1, 2, 3], device=DEV), k, v, table, ln)
     eff = [70, cap, 33]
-    check_rows(out, lse, q, k, v, table, eff, [(b, b, n - 1) for b, n in enumerate(eff)], 0.125, 0, 0)
+    check_rows(out, lse, q, k, v, table, eff, [(b, b, n - 1) for b, n in enumerate(eff)], 0.125, 0, 0,
+               scaled_v=kind == "prefill")
     ln[1] = -3
     if kind == "decode":
         out, lse = fp8q.paged_attention_decode(q, k, v, table, ln)
@@ -240,7 +242,7 @@ def test_row_scales_of_very_different_size(spread):
     out, lse = fp8q.paged_attention_decode(q, k, v, table, ln)
     check_rows(out, lse, q, k, v, table, lens, [(0, 0, 259)], 128 ** -0.5, 0, 0)
     o2, l2 = fp8q.paged_attention_prefill(q, torch.tensor([0, 1], device=DEV), k, v, table, ln)
-    check_rows(o2, l2, q, k, v, table, lens, [(0, 0, 259)], 128 ** -0.5, 0, 0)
+    check_rows(o2, l2, q, k, v, table, lens, [(0, 0, 259)], 128 ** -0.5, 0, 0, scaled_v=True)
 
 
 @pytest.mark.parametrize("qscale", [1e-30, 1e30])
@@ -252,7 +254,7 @@ def test_queries_of_extreme_size(qscale):
     out, lse = fp8q.paged_attention_decode(q, k, v, table, ln, softmax_scale=s)
     check_rows(out, lse, q, k, v, table, lens, [(0, 0, 89)], float(torch.tensor(s)), 0, 0)
     out, lse = fp8q.paged_attention_prefill(q, torch.tensor([0, 1], device=DEV), k, v, table, ln, softmax_scale=s)
-    check_rows(out, lse, q, k, v, table, lens, [(0, 0, 89)], float(torch.tensor(s)), 0, 0)
+    check_rows(out, lse, q, k, v, table, lens, [(0, 0, 89)], float(torch.tensor(s)), 0, 0, scaled_v=True)
 
 
 def test_queries_inside_a_fused_projection_and_other_streams():
@@ -270,7 +272,7 @@ def test_queries_inside_a_fused_projection_and_other_streams():
     torch.cuda.current_stream().wait_stream(s)
     rows = [(i, i, n - 1) for i, n in enumerate(lens)]
     check_rows(out, lse, q, k, v, table, lens, rows, 0.125, 0, 0)
-    check_rows(o2, l2, q, k, v, table, lens, rows, 0.125, 0, 0)
+    check_rows(o2, l2, q, k, v, table, lens, rows, 0.125, 0, 0, scaled_v=True)
 
 
 def test_calls_repeat_bit_for_bit_and_replay_in_a_graph_with_new_lengths():
@@ -445,7 +447,7 @@ def test_a_sequence_lives_through_prefill_decode_eviction_and_decode():
     ln = torch.tensor([n0], dtype=torch.int32, device=DEV)
     q = inputs.normal_bf16((n0, H * G, Dh), 1.0, seed=7).to(DEV)
     out, lse = fp8q.paged_attention_prefill(q, torch.tensor([0, n0], device=DEV), k, v, table, ln)
-    check_rows(out, lse, q, k, v, table, [n0], [(t, 0, t) for t in range(n0)], scale, 0, 0)
+    check_rows(out, lse, q, k, v, table, [n0], [(t, 0, t) for t in range(n0)], scale, 0, 0, scaled_v=True)
     mass = torch.zeros((1, H, 128), device=DEV)
     n = n0
     total = torch.zeros((H, 128), dtype=torch.float64)
