@@ -215,20 +215,41 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
 __device__ __forceinline__ void arrive_release(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The MMA warp runs as a whole and one elected lane (`leader`) issues: with the
+// descriptors in a branch of lane 0 alone an MMA took 270 cycles to issue, four
+// times as long as it runs.  A descriptor is its low word (the address moves)
+// and a constant high word.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t l;
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(l));
+    return l;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc,
+                                       uint32_t acc, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(acc), "r"(leader)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, uint32_t acc,
+                                       uint32_t leader) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(acc), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t bar, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(leader)
         : "memory");
 }
 // 32 lanes x 16 columns from registers; tmem_st_wait() before they are read
@@ -300,17 +321,14 @@ __device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, 
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// MN-major operand (V: a row per position, 64 head elements of 128 bytes per
-// swizzled block): 8 positions 1 KiB apart, blocks `block` bytes apart.
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr, uint32_t block) {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(block >> 4) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
-    return d;
+// Low and high words of the shared-memory descriptors, 128-byte swizzle.  K-major
+// (Q, K): rows of 64 elements, 8 rows 1 KiB apart.  MN-major (V: a row per
+// position, 64 head elements of 128 bytes per block): 8 positions 1 KiB apart,
+// blocks `block` bytes apart.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t block) {
+    return ((addr >> 4) & 0x3FFFu) | (block ? (block >> 4) << 16 : 1u << 16);
 }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // stride; sm_100 version; 128-byte swizzle
 // kind::f16: fp32 sums, A and B fp16
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn) {
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
@@ -401,7 +419,8 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
 
     if (wg == 0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
+            const uint32_t leader = elect_one();
             // ------------------------------------------------------ MMAs --
             constexpr uint32_t id_s = idesc_f16(128, KT, false), id_o = idesc_f16(128, DH, true);
             uint32_t kc = 0, seg = 0, pc[2] = {0, 0};   // tiles so far; runs; P tiles so far
@@ -411,12 +430,13 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                 const uint32_t qa = sb + i * P::QB, ka = sb + P::OFF_K + buf * P::KVB;
 #pragma unroll
                 for (int blk = 0; blk < DH / 64; ++blk) {
-                    const uint64_t qd = sdesc_k_sw128(qa + blk * 128 * 128), kd = sdesc_k_sw128(ka + blk * KT * 128);
+                    const uint32_t qd = desc_lo(qa + blk * 128 * 128, 0), kd = desc_lo(ka + blk * KT * 128, 0);
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        mma_ss(tmem + i * P::S_COL, qd + 2 * s, kd + 2 * s, id_s, (blk | s) ? 1u : 0u);
+                        mma_ss(tmem + i * P::S_COL, qd + 2 * s, kDescHi, kd + 2 * s, kDescHi, id_s, (blk | s) ? 1u : 0u,
+                               leader);
                 }
-                tc_commit(sfull(i));
+                commit_one(sfull(i), leader);
             };
             while (ok && at < end) {
                 const int len = run_length(), tiles_m = u.rho1 - u.rho0 > 128 ? MT : 1;
@@ -425,19 +445,19 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                 if (!ok) break;
                 tc_fence_after();
                 for (int i = 0; i < tiles_m; ++i) issue_s(i, kc & 1);
-                tc_commit(kempty(kc & 1));
+                commit_one(kempty(kc & 1), leader);
                 for (int k = 0; ok && k < len; ++k, ++kc) {
                     ok = wait_for(vfull(kc & 1), (kc >> 1) & 1u, abort_flag, kErrMma);
                     for (int i = 0; ok && i < tiles_m; ++i) {
                         ok = wait_for(pfull(i), pc[i]++ & 1u, abort_flag, kErrMma);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t vd = sdesc_mn(sb + P::OFF_V + (kc & 1) * P::KVB, KT * 128);
+                        const uint32_t vd = desc_lo(sb + P::OFF_V + (kc & 1) * P::KVB, KT * 128);
 #pragma unroll
                         for (int s = 0; s < KT / 16; ++s)
-                            mma_ts(tmem + P::O_COL + i * DH, tmem + i * P::S_COL + 8 * s, vd + 128 * s, id_o,
-                                   (k | s) ? 1u : 0u);
-                        tc_commit(pvdone(i));
+                            mma_ts(tmem + P::O_COL + i * DH, tmem + i * P::S_COL + 8 * s, vd + 128 * s, kDescHi, id_o,
+                                   (k | s) ? 1u : 0u, leader);
+                        commit_one(pvdone(i), leader);
                         if (k + 1 < len) {
                             if (i == 0) ok = wait_for(kfull((kc + 1) & 1), ((kc + 1) >> 1) & 1u, abort_flag, kErrMma);
                             if (!ok) break;
@@ -446,13 +466,13 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                         }
                     }
                     if (!ok) break;
-                    tc_commit(vempty(kc & 1));
-                    if (k + 1 < len) tc_commit(kempty((kc + 1) & 1));
+                    commit_one(vempty(kc & 1), leader);
+                    if (k + 1 < len) commit_one(kempty((kc + 1) & 1), leader);
                 }
                 advance(len);
                 ++seg;
             }
-            tc_commit(drain);
+            commit_one(drain, leader);
             wait_bar_drain(drain, 0u);
         }
         __syncwarp();
