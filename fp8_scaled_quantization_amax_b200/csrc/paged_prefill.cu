@@ -16,7 +16,8 @@
 // 2^15 (then to 2^7 below the maximum), so O is seldom rescaled, and weights
 // are exact to 2^-11 down to 2^-21 of the largest in fp16.
 //
-// Warp roles: warp 0 issues the MMAs; warpgroups 1 and 2 are the softmax of the
+// Warp roles: warp 0 issues the MMAs; warps 1 to 3 look up the tiles' pages and
+// scales; warpgroups 1 and 2 are the softmax of the
 // two row tiles (and load Q, rescale O, write results); warpgroup 3 reads the
 // cache through the block table, converts and writes the K and V tiles (two
 // buffers each).  The tensor core alternates between the row tiles, so one
@@ -77,7 +78,7 @@ struct Pre {
     static constexpr int M_DK = 0, M_DV = KT * 4, M_SLOT = KT * 8, M_LIVE = KT * 12, M_MAX = M_LIVE + 16,
                          M_EXP = M_MAX + 16, M_BYTES = M_EXP + 16;
     static constexpr int OFF_BAR = OFF_M + META * M_BYTES;
-    static constexpr int NBARS = 8 + 4 * MT + 1;
+    static constexpr int NBARS = 8 + 4 * MT + 1 + META;
     static constexpr size_t SMEM = 1024 + OFF_BAR + NBARS * 8 + 64;
     static constexpr int S_COL = KT, O_COL = 256;         // TMEM: S of tile i at i * S_COL, O at O_COL + i * DH
     static constexpr int VC_E4M3 = 6, VC_E5M2 = -1;       // code * scale * 2^(VC - exponent of the largest) < 2^16
@@ -287,6 +288,11 @@ __device__ __forceinline__ uint64_t pack_ff(float lo, float hi) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
     return v;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 0 at -inf and below 2^-126
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -344,7 +350,8 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
     constexpr int MT = P::MT, KT = P::KT, ROWS = P::ROWS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint32_t s_tmem, s_abort, s_poison[8];
+    // s_poison: something was taken out of V (for good: later results of this CTA look again for nothing)
+    __shared__ uint32_t s_tmem, s_abort, s_poison;
     volatile uint32_t *abort_flag = &s_abort;
     const uint32_t sb = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
@@ -358,6 +365,7 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
     auto pfull = [&](int i) { return bar0 + 8 * (8 + 2 * MT + i); };
     auto pvdone = [&](int i) { return bar0 + 8 * (8 + 3 * MT + i); };
     const uint32_t drain = bar0 + 8 * (8 + 4 * MT);
+    auto mfull = [&](uint32_t k) { return bar0 + 8 * (9 + 4 * MT + k % P::META); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -372,8 +380,9 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
             mbar_init(sfull(i), 1);
             mbar_init(pvdone(i), 1);
         }
+        for (int i = 0; i < P::META; ++i) mbar_init(mfull(i), 32);
         mbar_init(drain, 1);
-        s_abort = 0u;
+        s_abort = s_poison = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -423,8 +432,7 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
             const uint32_t leader = elect_one();
             // ------------------------------------------------------ MMAs --
             constexpr uint32_t id_s = idesc_f16(128, KT, false), id_o = idesc_f16(128, DH, true);
-            uint32_t kc = 0, seg = 0, pc[2] = {0, 0};   // tiles so far; runs; P tiles so far
-            uint32_t qc[2] = {0, 0};
+            uint32_t kc = 0, pc[2] = {0, 0}, qc[2] = {0, 0};   // tiles so far; P tiles; runs
             bool ok = true;
             auto issue_s = [&](int i, uint32_t buf) {
                 const uint32_t qa = sb + i * P::QB, ka = sb + P::OFF_K + buf * P::KVB;
@@ -470,10 +478,53 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                     if (k + 1 < len) commit_one(kempty((kc + 1) & 1), leader);
                 }
                 advance(len);
-                ++seg;
             }
             commit_one(drain, leader);
             wait_bar_drain(drain, 0u);
+            __syncwarp();
+        } else {
+            // ------------------------- slots, scales and masks of tiles ---
+            // Warps 1 to 3 take turns, a few tiles ahead of the converter: a tile's look-up is two dependent
+            // loads, which nothing there could hide.
+            uint32_t kc = 0;
+            while (at < end) {
+                const int len = run_length();
+                for (int k = 0; k < len; ++k, ++kc) {
+                    // S of tile kc - 5 is issued behind the softmax of tile kc - 6: nobody reads kc - 8 any more.
+                    // Every warp waits for every tile: a parity only tells a phase from its neighbours.
+                    if (kc >= 5) wait_for(kempty((kc - 5) & 1), ((kc - 5) >> 1) & 1u, abort_flag, kErrProducer);
+                    if (kc % 3 != (uint32_t)(warp - 1)) continue;
+                    uint8_t *m = smem + P::OFF_M + (kc % P::META) * P::M_BYTES;
+                    const int j0 = tile_pos<KT>(u, tile + k);
+                    int s[KT / 32];
+                    float dk[KT / 32], dv[KT / 32];
+#pragma unroll
+                    for (int i = 0; i < KT / 32; ++i) {
+                        const int j = j0 + 32 * i + lane;
+                        s[i] = j < u.n && j <= u.pmax ? pv.slot(who.x, j) : -1;
+                    }
+#pragma unroll
+                    for (int i = 0; i < KT / 32; ++i) {
+                        dk[i] = s[i] >= 0 ? pv.ks[(int64_t)s[i] * pv.H + h] : 0.0f;
+                        dv[i] = s[i] >= 0 ? pv.vs[(int64_t)s[i] * pv.H + h] : 0.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < KT / 32; ++i) {
+                        reinterpret_cast<float *>(m + P::M_DK)[32 * i + lane] = dk[i];
+                        reinterpret_cast<float *>(m + P::M_DV)[32 * i + lane] = dv[i];
+                        reinterpret_cast<int *>(m + P::M_SLOT)[32 * i + lane] = s[i];
+                        const uint32_t live = __ballot_sync(0xFFFFFFFFu, s[i] >= 0);
+                        const float d = fabsf(dv[i]);
+                        const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, d < INFINITY ? __float_as_uint(d) : 0u);
+                        if (lane == 0) {
+                            reinterpret_cast<uint32_t *>(m + P::M_LIVE)[i] = live;
+                            reinterpret_cast<uint32_t *>(m + P::M_MAX)[i] = mx;
+                        }
+                    }
+                    arrive_release(mfull(kc));
+                }
+                advance(len);
+            }
         }
         __syncwarp();
     } else if (wg == 3) {
@@ -484,41 +535,19 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
         const int swap = (c >> 2) & 1;        // half the chunks are stored high half first: no bank conflicts
         const bool c_live = 16 * c < pv.Dh;
         const uint64_t row_bytes = (uint64_t)pv.H * pv.Dh;
-        uint32_t kc = 0, seg = 0;
+        uint32_t kc = 0;
         int ex = -1000;                       // exponent of the largest V scale of the run so far
-        auto wg_sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
         auto meta = [&](uint32_t k) { return smem + P::OFF_M + (k % P::META) * P::M_BYTES; };
-        // slots and scales of tile t (the k-th of this CTA) of unit u; head hh
-        auto look_up = [&](uint32_t k, int t, bool fresh) {
-            uint8_t *m = meta(k);
-            float dv = 0.0f;
-            if (tid < KT) {
-                const int j = tile_pos<KT>(u, t) + tid;
-                const int s = j < u.n && j <= u.pmax ? pv.slot(who.x, j) : -1;
-                float dk = 0.0f;
-                if (s >= 0) {
-                    dk = pv.ks[(int64_t)s * pv.H + h];
-                    dv = pv.vs[(int64_t)s * pv.H + h];
-                }
-                reinterpret_cast<float *>(m + P::M_DK)[tid] = dk;
-                reinterpret_cast<float *>(m + P::M_DV)[tid] = dv;
-                reinterpret_cast<int *>(m + P::M_SLOT)[tid] = s;
-                const uint32_t live = __ballot_sync(0xFFFFFFFFu, s >= 0);
-                const float d = fabsf(dv);
-                const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, d < INFINITY ? __float_as_uint(d) : 0u);
-                if (lane == 0) {
-                    reinterpret_cast<uint32_t *>(m + P::M_LIVE)[w] = live;
-                    reinterpret_cast<uint32_t *>(m + P::M_MAX)[w] = mx;
-                }
-            }
-            if (fresh && tid == 0) s_poison[seg & 7] = 0u;
-            wg_sync();
+        // waits for the slots of the k-th tile; the exponent its V is held against
+        auto look_up = [&](uint32_t k, bool fresh) {
+            const uint8_t *m = meta(k);
+            wait_for(mfull(k), (k / P::META) & 1u, abort_flag, kErrProducer);
             uint32_t mx = 0;
 #pragma unroll
             for (int i = 0; i < KT / 32; ++i) mx = max(mx, reinterpret_cast<const uint32_t *>(m + P::M_MAX)[i]);
             if (fresh) ex = -1000;
             if (mx) ex = max(ex, max((int)(mx >> 23) - 127, -100));
-            if (tid == 0) *reinterpret_cast<int *>(m + P::M_EXP) = ex;
+            if (tid == 0) *reinterpret_cast<int *>(meta(k) + P::M_EXP) = ex;
         };
         auto load = [&](uint4 (&v)[ITS], const uint8_t *codes, uint32_t k) {
             const int *slot = reinterpret_cast<const int *>(meta(k) + P::M_SLOT);
@@ -542,7 +571,7 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
         };
         uint4 kv[ITS], vv[ITS];
         if (at < end) {
-            look_up(0, tile, true);
+            look_up(0, true);
             load(kv, pv.kc, 0);
             load(vv, pv.vc, 0);
         }
@@ -570,13 +599,11 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                 arrive_release(kfull(buf));
                 // ---- the next tile's slots, and its K on the way while V is converted
                 bool more = k + 1 < len;
-                const uint32_t this_seg = seg;
                 if (more) {
-                    look_up(kc + 1, tile + k + 1, false);
+                    look_up(kc + 1, false);
                 } else if (at + len < end) {
                     advance(len);
-                    ++seg;
-                    look_up(kc + 1, 0, true);
+                    look_up(kc + 1, true);
                     more = true;
                 } else {
                     at = end;
@@ -616,7 +643,7 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                     for (int e = 0; e < 8; ++e) x[e] = mul_f16x2(x[e], f2);
                     put(vb, row, x);
                 }
-                if (bad) s_poison[this_seg & 7] = 1u;
+                if (bad) s_poison = 1u;
                 fence_async();
                 arrive_release(vfull(buf));
                 if (more) load(vv, pv.vc, kc + 1);
@@ -632,14 +659,13 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
         const int mi = wg - 1, row = threadIdx.x - 128 * wg;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_base + mi * P::S_COL, to = tmem + lane_base + P::O_COL + mi * DH;
-        uint32_t kc = 0, sc = 0, seg = 0;     // tiles of the CTA; S tiles of this row tile; runs
+        uint32_t kc = 0, sc = 0;              // tiles of the CTA; S tiles of this row tile
         while (at < end) {
             const int len = run_length();
             const bool mine = mi == 0 || u.rho1 - u.rho0 > 128;
             if (!mine) {
                 kc += len;
                 advance(len);
-                ++seg;
                 continue;
             }
             const int rho = u.rho0 + mi * 128 + row;
@@ -682,95 +708,122 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                 const int j0 = tile_pos<KT>(u, tile + k);
                 wait_for(sfull(mi), sc & 1u, abort_flag, kErrEpilogue);
                 tc_fence_after();
-                uint32_t x[KT];
-#pragma unroll
-                for (int i = 0; i < KT / 32; ++i) tmem_ld32_async(ts + 32 * i, x + 32 * i);
-                tmem_ld_wait(x);
-                // ---- times K's scales
                 const float4 *dk = reinterpret_cast<const float4 *>(m + P::M_DK);
-#pragma unroll
-                for (int i = 0; i < KT / 4; ++i) {
-                    const float4 d = dk[i];
-                    const uint64_t lo = mul_f32x2(pack_f32x2(x[4 * i], x[4 * i + 1]), pack_ff(d.x, d.y));
-                    const uint64_t hi = mul_f32x2(pack_f32x2(x[4 * i + 2], x[4 * i + 3]), pack_ff(d.z, d.w));
-                    x[4 * i] = (uint32_t)lo;
-                    x[4 * i + 1] = (uint32_t)(lo >> 32);
-                    x[4 * i + 2] = (uint32_t)hi;
-                    x[4 * i + 3] = (uint32_t)(hi >> 32);
-                }
-                // ---- what the row does not see
                 const uint32_t *live = reinterpret_cast<const uint32_t *>(m + P::M_LIVE);
                 uint32_t all = 0xFFFFFFFFu;
 #pragma unroll
                 for (int i = 0; i < KT / 32; ++i) all &= live[i];
-                if (all != 0xFFFFFFFFu || !tile_full<KT>(pv, u, j0)) {
+                const bool masked = all != 0xFFFFFFFFu || !tile_full<KT>(pv, u, j0);
+                // 32 columns of S times K's scales; what the row does not see becomes -inf
+                auto columns = [&](uint32_t (&x)[32], int i) {
 #pragma unroll
-                    for (int i = 0; i < KT / 32; ++i) {
+                    for (int c = 0; c < 8; ++c) {
+                        const float4 d = dk[8 * i + c];
+                        const uint64_t lo = mul_f32x2(pack_f32x2(x[4 * c], x[4 * c + 1]), pack_ff(d.x, d.y));
+                        const uint64_t hi = mul_f32x2(pack_f32x2(x[4 * c + 2], x[4 * c + 3]), pack_ff(d.z, d.w));
+                        x[4 * c] = (uint32_t)lo;
+                        x[4 * c + 1] = (uint32_t)(lo >> 32);
+                        x[4 * c + 2] = (uint32_t)hi;
+                        x[4 * c + 3] = (uint32_t)(hi >> 32);
+                    }
+                    if (masked) {
                         const int c0 = j0 + 32 * i;
                         const uint32_t see = below(p + 1 - c0) & (~below(wb - c0) | below(pv.sinks - c0)) & live[i];
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
-                            if (!((see >> c) & 1u)) x[32 * i + c] = 0xFF800000u;   // -inf
+                            if (!((see >> c) & 1u)) x[c] = 0xFF800000u;   // -inf
                     }
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                };
+                auto largest = [](const uint32_t (&x)[32], float v) {
+                    float w = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < KT; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cf;
-                // ---- the reference, and O against it and V's exponent
-                const int ex_new = *reinterpret_cast<const int *>(m + P::M_EXP);
-                const bool up = top > mr + kAbove;
-                if (__any_sync(0xFFFFFFFFu, up) || ex_new != ex) {
-                    float al = 1.0f;
+                    for (int c = 0; c < 32; c += 4) {
+                        v = max3(v, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                        w = max3(w, __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
+                    }
+                    return fmaxf(v, w);
+                };
+                // The first tile's maximum sets the reference before any weight is taken.  Later tiles take their
+                // weights against the reference they find and look at the maximum afterwards: P waits in registers
+                // (S's columns become P's), and the few tiles that pass the reference by 2^15 are done again.
+                if (k == 0) {
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int i = 0; i < KT / 32; ++i) {
+                        uint32_t x[32];
+                        tmem_ld32_async(ts + 32 * i, x);
+                        tmem_ld_wait(x);
+                        columns(x, i);
+                        top = largest(x, top);
+                    }
+                    if (top * cf > kNoMax) mr = top * cf - kBelow;
+                }
+                uint32_t pk[KT / 2];
+                float al = 1.0f, sum, top;
+                while (true) {
+                    const uint64_t cf2 = pack_ff(cf, cf), mr2 = pack_ff(-mr, -mr);
+                    uint64_t acc = 0ull;
+                    top = -INFINITY;
+                    uint32_t xa[32], xb[32];
+                    tmem_ld32_async(ts, xa);
+#pragma unroll
+                    for (int i = 0; i < KT / 32; ++i) {
+                        auto &x = i & 1 ? xb : xa;
+                        auto &nx = i & 1 ? xa : xb;
+                        tmem_ld_wait(x);
+                        if (i + 1 < KT / 32) tmem_ld32_async(ts + 32 * (i + 1), nx);
+                        columns(x, i);
+                        top = largest(x, top);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const uint64_t e = fma_f32x2(pack_f32x2(x[2 * c], x[2 * c + 1]), cf2, mr2);
+                            float e0, e1;
+                            unpack_f32x2(e, e0, e1);
+                            e0 = exp2_fast(e0);
+                            e1 = exp2_fast(e1);
+                            acc = add_f32x2(acc, pack_ff(e0, e1));
+                            pk[16 * i + c] = pack_f16x2(e0, e1);
+                        }
+                    }
+                    float s0, s1;
+                    unpack_f32x2(acc, s0, s1);
+                    sum = s0 + s1;
+                    top *= cf;
+                    const bool up = top > mr + kAbove;
+                    if (!__any_sync(0xFFFFFFFFu, up)) break;
                     if (up) {
                         al = exp2_fast(mr - (top - kBelow));
-                        mr = top - kBelow;
-                        l *= al;
+                        mr = top == INFINITY ? top : top - kBelow;
                     }
-                    if (k > 0) {
-                        if (ex_new != ex) al *= ex > -1000 && ex - ex_new >= -126 ? pow2i(ex - ex_new) : 0.0f;
-                        wait_for(pvdone(mi), (sc - 1) & 1u, abort_flag, kErrEpilogue);
-                        tc_fence_after();
+                    if (__all_sync(0xFFFFFFFFu, !up || top == INFINITY)) break;   // infinite: NaN whatever is done
+                }
+                l = l * al + sum;
+                // ---- O against the new reference and V's exponent
+                const int ex_new = *reinterpret_cast<const int *>(m + P::M_EXP);
+                if (k > 0 && (__any_sync(0xFFFFFFFFu, al != 1.0f) || ex_new != ex)) {
+                    if (ex_new != ex) al *= ex > -1000 && ex - ex_new >= -126 ? pow2i(ex - ex_new) : 0.0f;
+                    wait_for(pvdone(mi), (sc - 1) & 1u, abort_flag, kErrEpilogue);
+                    tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < DH; c += 16) {
-                            uint32_t o[16];
-                            asm volatile(
-                                "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                                "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
-                                  "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]),
-                                  "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-                                : "r"(to + c));
-                            tmem_ld_wait(o);
+                    for (int c = 0; c < DH; c += 16) {
+                        uint32_t o[16];
+                        asm volatile(
+                            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                            : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
+                              "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
+                              "=r"(o[14]), "=r"(o[15])
+                            : "r"(to + c));
+                        tmem_ld_wait(o);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                            tmem_st16(to + c, o);
-                        }
-                        tmem_st_wait();
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                        tmem_st16(to + c, o);
                     }
-                    ex = ex_new;
                 }
-                // ---- P = exp2(x cf - mr), fp16, over S's columns
-                const uint64_t cf2 = pack_ff(cf, cf), mr2 = pack_ff(-mr, -mr);
-                uint64_t sum = 0ull;
+                ex = ex_new;
+                // ---- P over S's columns
 #pragma unroll
-                for (int i = 0; i < KT / 32; ++i) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const uint64_t e = fma_f32x2(pack_f32x2(x[32 * i + 2 * c], x[32 * i + 2 * c + 1]), cf2, mr2);
-                        float e0, e1;
-                        unpack_f32x2(e, e0, e1);
-                        e0 = exp2_fast(e0);
-                        e1 = exp2_fast(e1);
-                        sum = add_f32x2(sum, pack_ff(e0, e1));
-                        pk[c] = pack_f16x2(e0, e1);
-                    }
-                    tmem_st16(ts + 16 * i, pk);
-                }
-                float s0, s1;
-                unpack_f32x2(sum, s0, s1);
-                l += s0 + s1;
+                for (int i = 0; i < KT / 32; ++i) tmem_st16(ts + 16 * i, pk + 16 * i);
                 tmem_st_wait();
                 tc_fence_before();
                 arrive_release(pfull(mi));
@@ -789,7 +842,7 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
             const float fo = ex > -1000 ? pow2i(min(ex - vc, 127)) : 0.0f;
             const float r = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
             float *part = a.part + ((int64_t)blockIdx.x * 2 + (tile == 0 ? 1 : 0)) * ((int64_t)ROWS * (DH + 2));
-            const bool poison = s_poison[seg & 7] != 0u;
+            const bool poison = *reinterpret_cast<volatile uint32_t *>(&s_poison) != 0u;
 #pragma unroll 1
             for (int c = 0; c < DH; c += 32) {
                 uint32_t o[32];
@@ -849,7 +902,6 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                 }
             }
             advance(len);
-            ++seg;
         }
     }
 
