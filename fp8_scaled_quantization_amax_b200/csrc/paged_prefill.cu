@@ -9,12 +9,14 @@
 //   softmax     a thread per row, S in its registers; P back to TMEM as fp16;
 //   O += P V    P from TMEM, V from shared memory, O stays in TMEM.
 // E4M3 and E5M2 codes are exact in fp16.  K's row scales multiply the columns
-// of S in fp32; V's are multiplied into the fp16 V (one rounding of 2^-12),
-// against a running power of two of the largest scale so far.  Q's rows are
-// brought to [2^14, 2^15) by a power of two, exact in fp16 above 2^-24 of the
-// row's largest.  The softmax reference only moves when a logit passes it by
-// 2^15 (then to 2^7 below the maximum), so O is seldom rescaled, and weights
-// are exact to 2^-11 down to 2^-21 of the largest in fp16.
+// of S in fp32 (in the multiply-add that subtracts the reference); V's are
+// multiplied into the fp16 V (rounded to fp16 as a factor and as a product,
+// 2^-11 each: in P they would cost a multiply and a shared load per weight),
+// against a running power of two of the largest scale so far.  Q is brought to
+// [2^14, 2^15) by a power of two.  The softmax reference is set to 2^7 below a
+// maximum and only moves when a tile's weights sum to 2^15, so neither the
+// maximum of a tile is looked for nor O rescaled but seldom, and weights are
+// exact to 2^-11 down to 2^-21 of the largest in fp16.
 //
 // Warp roles: warp 0 issues the MMAs; warps 1 to 3 look up the tiles' pages and
 // scales; warpgroups 1 and 2 are the softmax of the
@@ -46,8 +48,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.0e38f;    // the reference before the first logit
-constexpr float kAbove = 15.0f;       // log2 of how far a logit may pass the reference
-constexpr float kBelow = 7.0f;        // log2 of how far under the maximum it is then set
+constexpr float kBelow = 7.0f;        // log2 of how far under the maximum a reference is set
+constexpr float kMaxSum = 32768.0f;   // a row's weights of one tile sum to less, so that none passes 2^15
 
 struct PrefillArgs {
     const __nv_bfloat16 *q;
@@ -77,7 +79,8 @@ struct Pre {
     static constexpr int OFF_K = MT * QB, OFF_V = OFF_K + 2 * KVB, OFF_M = OFF_V + 2 * KVB;
     static constexpr int M_DK = 0, M_DV = KT * 4, M_SLOT = KT * 8, M_LIVE = KT * 12, M_MAX = M_LIVE + 16,
                          M_EXP = M_MAX + 16, M_BYTES = M_EXP + 16;
-    static constexpr int OFF_BAR = OFF_M + META * M_BYTES;
+    static constexpr int OFF_F = OFF_M + META * M_BYTES;   // column factors: [row tile][2][KT]
+    static constexpr int OFF_BAR = OFF_F + MT * 2 * KT * 4;
     static constexpr int NBARS = 8 + 4 * MT + 1 + META;
     static constexpr size_t SMEM = 1024 + OFF_BAR + NBARS * 8 + 64;
     static constexpr int S_COL = KT, O_COL = 256;         // TMEM: S of tile i at i * S_COL, O at O_COL + i * DH
@@ -270,11 +273,6 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -287,11 +285,6 @@ __device__ __forceinline__ uint64_t pack_ff(float lo, float hi) {
     uint64_t v;
     asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
     return v;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
 }
 __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 0 at -inf and below 2^-126
     float r;
@@ -323,6 +316,19 @@ template <int FMT>
 __device__ __forceinline__ uint32_t nonfinite4(uint32_t c) {
     return ((c & 0x7F7F7F7Fu) + (FMT == FP8_E4M3 ? 0x01010101u : 0x04040404u)) & 0x80808080u;
 }
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void st_shared_u32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 __device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
@@ -351,7 +357,7 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // s_poison: something was taken out of V (for good: later results of this CTA look again for nothing)
-    __shared__ uint32_t s_tmem, s_abort, s_poison;
+    __shared__ uint32_t s_tmem, s_abort, s_poison, s_qmax[MT][4];
     volatile uint32_t *abort_flag = &s_abort;
     const uint32_t sb = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
@@ -510,7 +516,7 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                     }
 #pragma unroll
                     for (int i = 0; i < KT / 32; ++i) {
-                        reinterpret_cast<float *>(m + P::M_DK)[32 * i + lane] = dk[i];
+                        reinterpret_cast<float *>(m + P::M_DK)[32 * i + lane] = dk[i] * fabsf(a.scale) * kLog2e;
                         reinterpret_cast<float *>(m + P::M_DV)[32 * i + lane] = dv[i];
                         reinterpret_cast<int *>(m + P::M_SLOT)[32 * i + lane] = s[i];
                         const uint32_t live = __ballot_sync(0xFFFFFFFFu, s[i] >= 0);
@@ -534,29 +540,29 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
         const int tid = threadIdx.x - 384, w = tid >> 5, c = lane % CH, r0 = w * RPI + lane / CH;
         const int swap = (c >> 2) & 1;        // half the chunks are stored high half first: no bank conflicts
         const bool c_live = 16 * c < pv.Dh;
-        const uint64_t row_bytes = (uint64_t)pv.H * pv.Dh;
+        const uint32_t row_bytes = (uint32_t)(pv.H * pv.Dh);
         uint32_t kc = 0;
         int ex = -1000;                       // exponent of the largest V scale of the run so far
-        auto meta = [&](uint32_t k) { return smem + P::OFF_M + (k % P::META) * P::M_BYTES; };
+        auto meta = [&](uint32_t k) -> uint32_t { return sb + P::OFF_M + (k % P::META) * P::M_BYTES; };
         // waits for the slots of the k-th tile; the exponent its V is held against
         auto look_up = [&](uint32_t k, bool fresh) {
-            const uint8_t *m = meta(k);
             wait_for(mfull(k), (k / P::META) & 1u, abort_flag, kErrProducer);
             uint32_t mx = 0;
 #pragma unroll
-            for (int i = 0; i < KT / 32; ++i) mx = max(mx, reinterpret_cast<const uint32_t *>(m + P::M_MAX)[i]);
+            for (int i = 0; i < KT / 32; ++i) mx = max(mx, ld_shared_u32(meta(k) + P::M_MAX + 4 * i));
             if (fresh) ex = -1000;
             if (mx) ex = max(ex, max((int)(mx >> 23) - 127, -100));
-            if (tid == 0) *reinterpret_cast<int *>(meta(k) + P::M_EXP) = ex;
+            if (tid == 0) st_shared_u32(meta(k) + P::M_EXP, (uint32_t)ex);
         };
         auto load = [&](uint4 (&v)[ITS], const uint8_t *codes, uint32_t k) {
-            const int *slot = reinterpret_cast<const int *>(meta(k) + P::M_SLOT);
+            const uint32_t slots = meta(k) + P::M_SLOT + 4 * r0;
+            codes += h * pv.Dh + 16 * c;
 #pragma unroll
             for (int i = 0; i < ITS; ++i) {
-                const int s = slot[i * 4 * RPI + r0];
+                const int s = (int)ld_shared_u32(slots + i * 16 * RPI);
                 v[i] = make_uint4(0, 0, 0, 0);
                 if (s >= 0 && c_live)
-                    v[i] = *reinterpret_cast<const uint4 *>(codes + (uint64_t)(uint32_t)s * row_bytes + h * pv.Dh + 16 * c);
+                    v[i] = *reinterpret_cast<const uint4 *>(codes + (uint64_t)(uint32_t)s * row_bytes);
             }
         };
         auto put = [&](uint32_t base, int row, const uint32_t (&x)[8]) {
@@ -582,7 +588,7 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                 const int j0 = tile_pos<KT>(u, tile + k);
                 const bool full = tile_full<KT>(pv, u, j0);
                 const int my_ex = ex;
-                uint8_t *m = meta(kc);
+                const uint32_t dv = meta(kc) + P::M_DV + 4 * r0;
                 // ---- K
                 wait_for(kempty(buf), par, abort_flag, kErrProducer);
                 const uint32_t kb = sb + P::OFF_K + buf * P::KVB;
@@ -613,12 +619,11 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                 wait_for(vempty(buf), par, abort_flag, kErrProducer);
                 const uint32_t vb = sb + P::OFF_V + buf * P::KVB;
                 const float fp = my_ex > -1000 ? pow2i(max((FMT == FP8_E4M3 ? P::VC_E4M3 : P::VC_E5M2) - my_ex, -126)) : 0.0f;
-                const float *dv = reinterpret_cast<const float *>(m + P::M_DV);
                 uint32_t bad = 0;
 #pragma unroll
                 for (int i = 0; i < ITS; ++i) {
                     const int row = i * 4 * RPI + r0;
-                    float f = dv[row] * fp;
+                    float f = __uint_as_float(ld_shared_u32(dv + i * 16 * RPI)) * fp;
                     uint4 q = vv[i];
                     if (!full) {              // what only some rows see must be finite
                         const uint32_t nf = nonfinite4<FMT>(q.x) | nonfinite4<FMT>(q.y) | nonfinite4<FMT>(q.z) |
@@ -659,6 +664,8 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
         const int mi = wg - 1, row = threadIdx.x - 128 * wg;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_base + mi * P::S_COL, to = tmem + lane_base + P::O_COL + mi * DH;
+        auto wg_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(2 + mi) : "memory"); };
+        const uint32_t fbuf = sb + P::OFF_F + mi * 2 * KT * 4;
         uint32_t kc = 0, sc = 0;              // tiles of the CTA; S tiles of this row tile
         while (at < end) {
             const int len = run_length();
@@ -674,8 +681,9 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
             const int p = valid ? u.n - u.count + tok : -1;
             const int wb = p >= 0 ? pv.window_begin(p) : 0;
             const int64_t orow = (u.t0 + tok) * (int64_t)pv.H * a.G + (int64_t)h * a.G + g;
-            // ---- Q: this thread's row as fp16, by a power of two
-            float cf;
+            // ---- Q as fp16, by one power of two for the tile's 128 rows (an element loses something only below 2^-29
+            // of the tile's largest, and then 2^-40 of that in the logits)
+            float qf;
             {
                 const __nv_bfloat16 *qp = a.q + (u.t0 + tok) * a.ld_q + (int64_t)(h * a.G + g) * pv.Dh;
                 uint32_t mx = 0;
@@ -686,9 +694,13 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                         mx = amax_exact8(mx, *reinterpret_cast<const uint4 *>(qp + 8 * c), bad);
                     }
                 }
+                mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+                if (lane == 0) s_qmax[mi][warp & 3] = mx;
+                wg_sync();
+                mx = max(max(s_qmax[mi][0], s_qmax[mi][1]), max(s_qmax[mi][2], s_qmax[mi][3]));
                 const int e = max((int)(mx >> 7), 14) - 127;
                 const float up = a.scale < 0.0f ? -pow2i(14 - e) : pow2i(14 - e);   // the sign of the scale goes to Q
-                cf = fmaxf(fabsf(a.scale) * kLog2e * pow2i(e) * 0x1p-14f, 1e-37f);   // positive: -inf stays -inf
+                qf = pow2i(e) * 0x1p-14f;
                 const uint32_t qa = sb + mi * P::QB + row * 128;
 #pragma unroll
                 for (int c = 0; c < DH / 8; ++c) {
@@ -704,66 +716,64 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
             float mr = kNoMax, l = 0.0f;
             int ex = -1000;
             for (int k = 0; k < len; ++k, ++kc, ++sc) {
-                const uint8_t *m = smem + P::OFF_M + (kc % P::META) * P::M_BYTES;
+                const uint32_t m = sb + P::OFF_M + (kc % P::META) * P::M_BYTES, fk = fbuf + (kc & 1) * KT * 4;
                 const int j0 = tile_pos<KT>(u, tile + k);
-                wait_for(sfull(mi), sc & 1u, abort_flag, kErrEpilogue);
-                tc_fence_after();
-                const float4 *dk = reinterpret_cast<const float4 *>(m + P::M_DK);
-                const uint32_t *live = reinterpret_cast<const uint32_t *>(m + P::M_LIVE);
-                uint32_t all = 0xFFFFFFFFu;
+                // The columns' factors, before S is ready where their look-up can be waited for: from the second
+                // tile of a run on, when the one before it in the ring is known to be past (a parity only tells a
+                // phase from its neighbours); S of the first tile is behind its look-up.
+                if (k == 0) wait_for(sfull(mi), sc & 1u, abort_flag, kErrEpilogue);
+                else wait_for(mfull(kc), (kc / P::META) & 1u, abort_flag, kErrEpilogue);
+                if (row < KT)
+                    st_shared_u32(fk + 4 * row, __float_as_uint(__uint_as_float(ld_shared_u32(m + P::M_DK + 4 * row)) * qf));
+                wg_sync();
+                uint32_t live[KT / 32], all = 0xFFFFFFFFu;
 #pragma unroll
-                for (int i = 0; i < KT / 32; ++i) all &= live[i];
+                for (int i = 0; i < KT / 32; ++i) all &= live[i] = ld_shared_u32(m + P::M_LIVE + 4 * i);
                 const bool masked = all != 0xFFFFFFFFu || !tile_full<KT>(pv, u, j0);
-                // 32 columns of S times K's scales; what the row does not see becomes -inf
-                auto columns = [&](uint32_t (&x)[32], int i) {
+                if (k > 0) wait_for(sfull(mi), sc & 1u, abort_flag, kErrEpilogue);
+                tc_fence_after();
+                // what the row does not see of 32 columns
+                auto hide = [&](uint32_t (&x)[32], int i) {
+                    const int c0 = j0 + 32 * i;
+                    const uint32_t see = below(p + 1 - c0) & (~below(wb - c0) | below(pv.sinks - c0)) & live[i];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float4 d = dk[8 * i + c];
-                        const uint64_t lo = mul_f32x2(pack_f32x2(x[4 * c], x[4 * c + 1]), pack_ff(d.x, d.y));
-                        const uint64_t hi = mul_f32x2(pack_f32x2(x[4 * c + 2], x[4 * c + 3]), pack_ff(d.z, d.w));
-                        x[4 * c] = (uint32_t)lo;
-                        x[4 * c + 1] = (uint32_t)(lo >> 32);
-                        x[4 * c + 2] = (uint32_t)hi;
-                        x[4 * c + 3] = (uint32_t)(hi >> 32);
-                    }
-                    if (masked) {
-                        const int c0 = j0 + 32 * i;
-                        const uint32_t see = below(p + 1 - c0) & (~below(wb - c0) | below(pv.sinks - c0)) & live[i];
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!((see >> c) & 1u)) x[c] = 0xFF800000u;   // -inf
-                    }
-                };
-                auto largest = [](const uint32_t (&x)[32], float v) {
-                    float w = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        v = max3(v, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-                        w = max3(w, __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
-                    }
-                    return fmaxf(v, w);
+                    for (int c = 0; c < 32; ++c)
+                        if (!((see >> c) & 1u)) x[c] = 0xFF800000u;   // -inf
                 };
                 // The first tile's maximum sets the reference before any weight is taken.  Later tiles take their
-                // weights against the reference they find and look at the maximum afterwards: P waits in registers
-                // (S's columns become P's), and the few tiles that pass the reference by 2^15 are done again.
-                if (k == 0) {
-                    float top = -INFINITY;
-#pragma unroll 1
-                    for (int i = 0; i < KT / 32; ++i) {
-                        uint32_t x[32];
-                        tmem_ld32_async(ts + 32 * i, x);
-                        tmem_ld_wait(x);
-                        columns(x, i);
-                        top = largest(x, top);
-                    }
-                    if (top * cf > kNoMax) mr = top * cf - kBelow;
-                }
+                // weights against the reference they find, and their sum tells afterwards whether one may have passed
+                // 2^15: P waits in registers (S's columns become P's), and such a tile is done again.
                 uint32_t pk[KT / 2];
-                float al = 1.0f, sum, top;
+                float al = 1.0f, sum = 0.0f;
+                bool first = k == 0, bad = first;
                 while (true) {
-                    const uint64_t cf2 = pack_ff(cf, cf), mr2 = pack_ff(-mr, -mr);
-                    uint64_t acc = 0ull;
-                    top = -INFINITY;
+                    if (__any_sync(0xFFFFFFFFu, bad)) {
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int i = 0; i < KT / 32; ++i) {
+                            uint32_t x[32];
+                            tmem_ld32_async(ts + 32 * i, x);
+                            tmem_ld_wait(x);
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4) {
+                                const float4 f = ld_shared_f4(fk + 4 * (32 * i + c));
+                                x[c] = __float_as_uint(__uint_as_float(x[c]) * f.x);
+                                x[c + 1] = __float_as_uint(__uint_as_float(x[c + 1]) * f.y);
+                                x[c + 2] = __float_as_uint(__uint_as_float(x[c + 2]) * f.z);
+                                x[c + 3] = __float_as_uint(__uint_as_float(x[c + 3]) * f.w);
+                            }
+                            if (masked) hide(x, i);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) top = fmaxf(top, __uint_as_float(x[c]));
+                        }
+                        if (bad && top > kNoMax) {
+                            al = exp2_fast(mr - (top - kBelow));
+                            mr = top - kBelow;
+                        }
+                        first = true;
+                    }
+                    const uint64_t mr2 = pack_ff(-mr, -mr);
+                    uint64_t acc[2] = {0ull, 0ull};
                     uint32_t xa[32], xb[32];
                     tmem_ld32_async(ts, xa);
 #pragma unroll
@@ -772,34 +782,34 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                         auto &nx = i & 1 ? xa : xb;
                         tmem_ld_wait(x);
                         if (i + 1 < KT / 32) tmem_ld32_async(ts + 32 * (i + 1), nx);
-                        columns(x, i);
-                        top = largest(x, top);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 f = ld_shared_f4(fk + 4 * (32 * i + c));
+                            const uint64_t lo = fma_f32x2(pack_f32x2(x[c], x[c + 1]), pack_ff(f.x, f.y), mr2);
+                            const uint64_t hi = fma_f32x2(pack_f32x2(x[c + 2], x[c + 3]), pack_ff(f.z, f.w), mr2);
+                            x[c] = (uint32_t)lo;
+                            x[c + 1] = (uint32_t)(lo >> 32);
+                            x[c + 2] = (uint32_t)hi;
+                            x[c + 3] = (uint32_t)(hi >> 32);
+                        }
+                        if (masked) hide(x, i);
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {
-                            const uint64_t e = fma_f32x2(pack_f32x2(x[2 * c], x[2 * c + 1]), cf2, mr2);
-                            float e0, e1;
-                            unpack_f32x2(e, e0, e1);
-                            e0 = exp2_fast(e0);
-                            e1 = exp2_fast(e1);
-                            acc = add_f32x2(acc, pack_ff(e0, e1));
+                            const float e0 = exp2_fast(__uint_as_float(x[2 * c]));
+                            const float e1 = exp2_fast(__uint_as_float(x[2 * c + 1]));
+                            acc[c & 1] = add_f32x2(acc[c & 1], pack_ff(e0, e1));
                             pk[16 * i + c] = pack_f16x2(e0, e1);
                         }
                     }
                     float s0, s1;
-                    unpack_f32x2(acc, s0, s1);
+                    unpack_f32x2(add_f32x2(acc[0], acc[1]), s0, s1);
                     sum = s0 + s1;
-                    top *= cf;
-                    const bool up = top > mr + kAbove;
-                    if (!__any_sync(0xFFFFFFFFu, up)) break;
-                    if (up) {
-                        al = exp2_fast(mr - (top - kBelow));
-                        mr = top == INFINITY ? top : top - kBelow;
-                    }
-                    if (__all_sync(0xFFFFFFFFu, !up || top == INFINITY)) break;   // infinite: NaN whatever is done
+                    bad = !(sum < kMaxSum);
+                    if (first || !__any_sync(0xFFFFFFFFu, bad)) break;   // a second NaN or infinity is the result
                 }
                 l = l * al + sum;
                 // ---- O against the new reference and V's exponent
-                const int ex_new = *reinterpret_cast<const int *>(m + P::M_EXP);
+                const int ex_new = (int)ld_shared_u32(m + P::M_EXP);
                 if (k > 0 && (__any_sync(0xFFFFFFFFu, al != 1.0f) || ex_new != ex)) {
                     if (ex_new != ex) al *= ex > -1000 && ex - ex_new >= -126 ? pow2i(ex - ex_new) : 0.0f;
                     wait_for(pvdone(mi), (sc - 1) & 1u, abort_flag, kErrEpilogue);
