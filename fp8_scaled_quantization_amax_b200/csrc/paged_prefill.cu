@@ -27,9 +27,9 @@
 //
 // Split: k_prefill_plan lists the row blocks of all sequences and deals the
 // (row block, head, position tile) triples, laid end to end, to the CTAs in
-// equal runs.  A unit that one CTA covers is written at once; the others leave
-// (O, reference, sum) in the workspace and k_prefill_join adds the parts in the
-// order of the CTAs.
+// runs of equal cost.  A unit that one CTA covers is written at once; the others
+// leave (O, reference, sum) in the workspace and k_prefill_join adds the parts in
+// the order of the CTAs.
 //
 // What a row must not see is kept out of it whatever it holds: S is masked by
 // selection; V rows of slots that are no live position are written as zeros;
@@ -62,11 +62,11 @@ struct PrefillArgs {
     __nv_bfloat16 *out;
     float *lse;               // or nullptr
     float *part;              // two parts per CTA
-    int2 *span;               // per unit: first and last CTA
-    int64_t *hdr;             // {tiles in all, row blocks}
-    int64_t *first_block;     // [B + 1] row blocks before each sequence
+    int4 *split;              // per CTA: {row block, head, last CTA} of the unit that it began and others go on with
+    int64_t *hdr;             // {cost in all}
+    int64_t *first_block;     // [B] row blocks before each sequence
     int2 *block;              // {sequence, row block of it}
-    longlong2 *start;         // per CTA: {row block, tiles before it}
+    longlong2 *start;         // per CTA: {row block, cost before it}
 };
 
 template <int DH>
@@ -132,6 +132,10 @@ __device__ __forceinline__ bool tile_full(const PagedView &pv, const Unit &u, in
     return u.pmin >= 0 && j0 + KT - 1 <= u.pmin && (j0 >= pv.window_begin(u.pmax) || j0 + KT <= pv.sinks);
 }
 
+// A unit costs its tiles and this many more, for Q and the results.  Laid end to
+// end in cost, a unit's first kUnitCost places hold no tile.
+constexpr int kUnitCost = 3;
+
 constexpr int kPlanThreads = 1024;
 __device__ int64_t plan_scan(int64_t v, int64_t *buf, int64_t *total) {   // exclusive, block-wide
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -184,17 +188,14 @@ k_prefill_plan(const PagedView pv, const PrefillArgs a) {
             if (a.first_block[mid] <= i) lo = mid; else hi = mid - 1;
         }
         *who = make_int2(lo, (int)(i - a.first_block[lo]));
-        return (int64_t)unit_of<ROWS, KT>(pv, a, lo, who->y).tiles * pv.H;
+        return (int64_t)(unit_of<ROWS, KT>(pv, a, lo, who->y).tiles + kUnitCost) * pv.H;
     };
     int64_t sum = 0, total;
     int2 who = make_int2(0, 0);
     int64_t mine = 0;
     for (int64_t i = threadIdx.x; i < nb; i += kPlanThreads) sum += mine = tiles_at(i, &who);
     plan_scan(sum, buf, &total);
-    if (threadIdx.x == 0) {
-        a.hdr[0] = total;
-        a.hdr[1] = nb;
-    }
+    if (threadIdx.x == 0) a.hdr[0] = total;
     const int64_t n = min((int64_t)a.ctas, total);
     base = 0;
     for (int64_t i0 = 0; i0 < nb; i0 += kPlanThreads) {
@@ -204,12 +205,74 @@ k_prefill_plan(const PagedView pv, const PrefillArgs a) {
         base += all;
         if (i < nb) {
             a.block[i] = who;
-            // the CTAs whose first tile, total * c / n, lies here
+            // the CTAs whose first place, total * c / n, lies here
             for (int64_t c = (pre * n + total - 1) / total; c < n && total * c / n < pre + mine; ++c)
                 a.start[c] = make_longlong2(i, pre);
         }
     }
 }
+
+// The runs of one CTA: consecutive tiles of one unit.
+template <int ROWS, int KT>
+struct Runs {
+    const PagedView &pv;
+    const PrefillArgs &a;
+    int64_t at, end, total, ncta;     // places of the CTA; in all; CTAs with any
+    int2 who;
+    Unit u;
+    int bi, h, v, tile, len, span;    // row block, head, place in the unit; tiles [tile, tile + len) of it; places
+
+    __device__ __forceinline__ Runs(const PagedView &pv_, const PrefillArgs &a_) : pv(pv_), a(a_) {
+        total = a.hdr[0];
+        ncta = min((int64_t)a.ctas, total);
+        at = end = 0;
+        len = span = 0;
+        if ((int64_t)blockIdx.x >= ncta) return;
+        at = total * blockIdx.x / ncta;
+        end = total * (blockIdx.x + 1) / ncta;
+        const longlong2 s = a.start[blockIdx.x];
+        bi = (int)s.x;
+        who = a.block[bi];
+        u = unit_of<ROWS, KT>(pv, a, who.x, who.y);
+        const int places = u.tiles + kUnitCost;
+        h = (int)((at - s.y) / places);
+        v = (int)((at - s.y) % places);
+        settle();
+    }
+    __device__ __forceinline__ void cut() {
+        span = (int)min((int64_t)(u.tiles + kUnitCost - v), end - at);
+        tile = max(0, v - kUnitCost);
+        len = max(0, v + span - kUnitCost) - tile;
+    }
+    __device__ __forceinline__ void step() {
+        at += span;
+        v = 0;
+        if (at < end && ++h == pv.H) {
+            h = 0;
+            who = a.block[++bi];
+            u = unit_of<ROWS, KT>(pv, a, who.x, who.y);
+        }
+    }
+    __device__ __forceinline__ void settle() {          // to a run with tiles
+        while (at < end) {
+            cut();
+            if (len > 0) return;
+            step();
+        }
+        len = 0;
+    }
+    __device__ __forceinline__ void next() {
+        step();
+        settle();
+    }
+    __device__ __forceinline__ bool live() const { return len > 0; }
+    __device__ __forceinline__ bool whole() const { return tile == 0 && len == u.tiles; }
+    // CTA that holds the unit's last place: the largest c with total * c / ncta <= place
+    __device__ __forceinline__ int last_cta() const {
+        const int64_t place = at - v + u.tiles + kUnitCost - 1;
+        return (int)((place * ncta + ncta - 1) / total);
+    }
+};
 
 // --------------------------------------------------------------- PTX glue --
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag, uint32_t code) {
@@ -403,34 +466,8 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
     const uint32_t tmem = s_tmem;
     pdl_wait();
 
-    // this CTA's run of tiles
-    const int64_t total = a.hdr[0], ncta = min((int64_t)a.ctas, total);
-    const bool active = (int64_t)blockIdx.x < ncta;
-    int64_t at = 0, end = 0;
-    int bi = 0, h = 0, tile = 0;      // row block, head, tile in the unit
-    int2 who = make_int2(0, 0);
-    Unit u = {};
-    if (active) {
-        at = total * blockIdx.x / ncta;
-        end = total * (blockIdx.x + 1) / ncta;
-        const longlong2 s = a.start[blockIdx.x];
-        bi = (int)s.x;
-        who = a.block[bi];
-        u = unit_of<ROWS, KT>(pv, a, who.x, who.y);
-        h = (int)((at - s.y) / u.tiles);
-        tile = (int)((at - s.y) % u.tiles);
-    }
-    // to the next unit, after `done` tiles of this one
-    auto advance = [&](int done) {
-        at += done;
-        tile = 0;
-        if (at < end && ++h == pv.H) {
-            h = 0;
-            who = a.block[++bi];
-            u = unit_of<ROWS, KT>(pv, a, who.x, who.y);
-        }
-    };
-    auto run_length = [&] { return (int)min((int64_t)(u.tiles - tile), end - at); };
+    Runs<ROWS, KT> run(pv, a);
+    if (threadIdx.x == 128) a.split[blockIdx.x] = make_int4(-1, 0, 0, 0);   // the thread that writes the other value
 
     if (wg == 0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
@@ -452,8 +489,8 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                 }
                 commit_one(sfull(i), leader);
             };
-            while (ok && at < end) {
-                const int len = run_length(), tiles_m = u.rho1 - u.rho0 > 128 ? MT : 1;
+            for (; ok && run.live(); run.next()) {
+                const int len = run.len, tiles_m = run.u.rho1 - run.u.rho0 > 128 ? MT : 1;
                 for (int i = 0; ok && i < tiles_m; ++i) ok = wait_for(qfull(i), qc[i]++ & 1u, abort_flag, kErrMma);
                 ok = ok && wait_for(kfull(kc & 1), (kc >> 1) & 1u, abort_flag, kErrMma);
                 if (!ok) break;
@@ -483,7 +520,6 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                     commit_one(vempty(kc & 1), leader);
                     if (k + 1 < len) commit_one(kempty((kc + 1) & 1), leader);
                 }
-                advance(len);
             }
             commit_one(drain, leader);
             wait_bar_drain(drain, 0u);
@@ -493,21 +529,22 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
             // Warps 1 to 3 take turns, a few tiles ahead of the converter: a tile's look-up is two dependent
             // loads, which nothing there could hide.
             uint32_t kc = 0;
-            while (at < end) {
-                const int len = run_length();
-                for (int k = 0; k < len; ++k, ++kc) {
+            for (; run.live(); run.next()) {
+                const Unit &u = run.u;
+                const int h = run.h;
+                for (int k = 0; k < run.len; ++k, ++kc) {
                     // S of tile kc - 5 is issued behind the softmax of tile kc - 6: nobody reads kc - 8 any more.
                     // Every warp waits for every tile: a parity only tells a phase from its neighbours.
                     if (kc >= 5) wait_for(kempty((kc - 5) & 1), ((kc - 5) >> 1) & 1u, abort_flag, kErrProducer);
                     if (kc % 3 != (uint32_t)(warp - 1)) continue;
                     uint8_t *m = smem + P::OFF_M + (kc % P::META) * P::M_BYTES;
-                    const int j0 = tile_pos<KT>(u, tile + k);
+                    const int j0 = tile_pos<KT>(u, run.tile + k);
                     int s[KT / 32];
                     float dk[KT / 32], dv[KT / 32];
 #pragma unroll
                     for (int i = 0; i < KT / 32; ++i) {
                         const int j = j0 + 32 * i + lane;
-                        s[i] = j < u.n && j <= u.pmax ? pv.slot(who.x, j) : -1;
+                        s[i] = j < u.n && j <= u.pmax ? pv.slot(run.who.x, j) : -1;
                     }
 #pragma unroll
                     for (int i = 0; i < KT / 32; ++i) {
@@ -529,7 +566,6 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                     }
                     arrive_release(mfull(kc));
                 }
-                advance(len);
             }
         }
         __syncwarp();
@@ -556,7 +592,7 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
         };
         auto load = [&](uint4 (&v)[ITS], const uint8_t *codes, uint32_t k) {
             const uint32_t slots = meta(k) + P::M_SLOT + 4 * r0;
-            codes += h * pv.Dh + 16 * c;
+            codes += run.h * pv.Dh + 16 * c;
 #pragma unroll
             for (int i = 0; i < ITS; ++i) {
                 const int s = (int)ld_shared_u32(slots + i * 16 * RPI);
@@ -576,17 +612,16 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
             }
         };
         uint4 kv[ITS], vv[ITS];
-        if (at < end) {
+        if (run.live()) {
             look_up(0, true);
             load(kv, pv.kc, 0);
             load(vv, pv.vc, 0);
         }
-        while (at < end) {
-            const int len = run_length();
-            for (int k = 0; k < len; ++k, ++kc) {
+        int k = 0;                            // tile of the run
+        for (; run.live(); ++kc) {
+            {
                 const uint32_t buf = kc & 1, par = ((kc >> 1) & 1u) ^ 1u;
-                const int j0 = tile_pos<KT>(u, tile + k);
-                const bool full = tile_full<KT>(pv, u, j0);
+                const bool full = tile_full<KT>(pv, run.u, tile_pos<KT>(run.u, run.tile + k));
                 const int my_ex = ex;
                 const uint32_t dv = meta(kc) + P::M_DV + 4 * r0;
                 // ---- K
@@ -604,16 +639,11 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                 fence_async();
                 arrive_release(kfull(buf));
                 // ---- the next tile's slots, and its K on the way while V is converted
-                bool more = k + 1 < len;
-                if (more) {
-                    look_up(kc + 1, false);
-                } else if (at + len < end) {
-                    advance(len);
-                    look_up(kc + 1, true);
-                    more = true;
-                } else {
-                    at = end;
-                }
+                const bool fresh = k + 1 == run.len;
+                if (fresh) run.next();
+                k = fresh ? 0 : k + 1;
+                const bool more = run.live();
+                if (more) look_up(kc + 1, fresh);
                 if (more) load(kv, pv.kc, kc + 1);
                 // ---- V, scaled
                 wait_for(vempty(buf), par, abort_flag, kErrProducer);
@@ -652,10 +682,6 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                 fence_async();
                 arrive_release(vfull(buf));
                 if (more) load(vv, pv.vc, kc + 1);
-                if (k + 1 == len && more) {   // advanced already: the next run begins
-                    ++kc;
-                    break;
-                }
             }
         }
     } else if (wg - 1 < MT) {
@@ -667,52 +693,64 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
         auto wg_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(2 + mi) : "memory"); };
         const uint32_t fbuf = sb + P::OFF_F + mi * 2 * KT * 4;
         uint32_t kc = 0, sc = 0;              // tiles of the CTA; S tiles of this row tile
-        while (at < end) {
-            const int len = run_length();
-            const bool mine = mi == 0 || u.rho1 - u.rho0 > 128;
-            if (!mine) {
-                kc += len;
-                advance(len);
-                continue;
+        // the rows of this row tile in the run; Q as fp16
+        int p = -1, wb = 0;
+        int64_t orow = 0;
+        bool valid = false;
+        float qf = 0.0f;
+        auto mine = [&] { return mi == 0 || run.u.rho1 - run.u.rho0 > 128; };
+        auto find = [&] {                     // on to a run of this row tile
+            while (run.live() && !mine()) {
+                kc += run.len;
+                run.next();
             }
-            const int rho = u.rho0 + mi * 128 + row;
-            const bool valid = rho < u.rho1;
-            const int tok = rho / a.G, g = rho - tok * a.G;
-            const int p = valid ? u.n - u.count + tok : -1;
-            const int wb = p >= 0 ? pv.window_begin(p) : 0;
-            const int64_t orow = (u.t0 + tok) * (int64_t)pv.H * a.G + (int64_t)h * a.G + g;
-            // ---- Q as fp16, by one power of two for the tile's 128 rows (an element loses something only below 2^-29
-            // of the tile's largest, and then 2^-40 of that in the logits)
-            float qf;
-            {
-                const __nv_bfloat16 *qp = a.q + (u.t0 + tok) * a.ld_q + (int64_t)(h * a.G + g) * pv.Dh;
-                uint32_t mx = 0;
-#pragma unroll
-                for (int c = 0; c < DH / 8; ++c) {
-                    if (valid && 8 * c < pv.Dh) {
-                        uint32_t bad = 0;
-                        mx = amax_exact8(mx, *reinterpret_cast<const uint4 *>(qp + 8 * c), bad);
-                    }
-                }
-                mx = __reduce_max_sync(0xFFFFFFFFu, mx);
-                if (lane == 0) s_qmax[mi][warp & 3] = mx;
-                wg_sync();
-                mx = max(max(s_qmax[mi][0], s_qmax[mi][1]), max(s_qmax[mi][2], s_qmax[mi][3]));
-                const int e = max((int)(mx >> 7), 14) - 127;
-                const float up = a.scale < 0.0f ? -pow2i(14 - e) : pow2i(14 - e);   // the sign of the scale goes to Q
-                qf = pow2i(e) * 0x1p-14f;
-                const uint32_t qa = sb + mi * P::QB + row * 128;
-#pragma unroll
-                for (int c = 0; c < DH / 8; ++c) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (valid && 8 * c < pv.Dh) v = *reinterpret_cast<const uint4 *>(qp + 8 * c);
-                    st_shared16(qa + (c >> 3) * (128 * 128) + (((c & 7) ^ (row & 7)) << 4),
-                                pack_f16x2(bf_lo(v.x) * up, bf_hi(v.x) * up), pack_f16x2(bf_lo(v.y) * up, bf_hi(v.y) * up),
-                                pack_f16x2(bf_lo(v.z) * up, bf_hi(v.z) * up), pack_f16x2(bf_lo(v.w) * up, bf_hi(v.w) * up));
-                }
-                fence_async();
-                arrive_release(qfull(mi));
+        };
+        auto load_q = [&] {
+            const Unit &u = run.u;
+            const int rho = u.rho0 + mi * 128 + row, tok = rho / a.G, g = rho - tok * a.G;
+            valid = rho < u.rho1;
+            p = valid ? u.n - u.count + tok : -1;
+            wb = p >= 0 ? pv.window_begin(p) : 0;
+            orow = (u.t0 + tok) * (int64_t)pv.H * a.G + (int64_t)run.h * a.G + g;
+            // One power of two for the tile's 128 rows (an element loses something only below 2^-29 of the tile's
+            // largest, and then 2^-40 of that in the logits).
+            const __nv_bfloat16 *qp = a.q + (u.t0 + tok) * a.ld_q + (int64_t)(run.h * a.G + g) * pv.Dh;
+            uint32_t mx = 0;
+#pragma unroll 8
+            for (int c = 0; c < DH / 8; ++c)
+                if (valid && 8 * c < pv.Dh) mx = amax_fast8(mx, *reinterpret_cast<const uint4 *>(qp + 8 * c));
+            mx = amax_fast_final(mx);
+            if (mx == 0xFFFFFFFFu) {          // a NaN or infinity: the finite elements' maximum
+                mx = 0;
+                uint32_t bad = 0;
+#pragma unroll 1
+                for (int c = 0; c < DH / 8; ++c)
+                    if (8 * c < pv.Dh) mx = amax_exact8(mx, *reinterpret_cast<const uint4 *>(qp + 8 * c), bad);
             }
+            mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+            if (lane == 0) s_qmax[mi][warp & 3] = mx;
+            wg_sync();
+            mx = max(max(s_qmax[mi][0], s_qmax[mi][1]), max(s_qmax[mi][2], s_qmax[mi][3]));
+            const int e = max((int)(mx >> 7), 14) - 127;
+            const float up = a.scale < 0.0f ? -pow2i(14 - e) : pow2i(14 - e);   // the sign of the scale goes to Q
+            qf = pow2i(e) * 0x1p-14f;
+            const uint32_t qa = sb + mi * P::QB + row * 128;
+#pragma unroll 4
+            for (int c = 0; c < DH / 8; ++c) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (valid && 8 * c < pv.Dh) v = *reinterpret_cast<const uint4 *>(qp + 8 * c);
+                st_shared16(qa + (c >> 3) * (128 * 128) + (((c & 7) ^ (row & 7)) << 4),
+                            pack_f16x2(bf_lo(v.x) * up, bf_hi(v.x) * up), pack_f16x2(bf_lo(v.y) * up, bf_hi(v.y) * up),
+                            pack_f16x2(bf_lo(v.z) * up, bf_hi(v.z) * up), pack_f16x2(bf_lo(v.w) * up, bf_hi(v.w) * up));
+            }
+            fence_async();
+            arrive_release(qfull(mi));
+        };
+        find();
+        if (run.live()) load_q();
+        while (run.live()) {
+            const Unit u = run.u;
+            const int tile = run.tile, len = run.len;
             float mr = kNoMax, l = 0.0f;
             int ex = -1000;
             for (int k = 0; k < len; ++k, ++kc, ++sc) {
@@ -838,16 +876,18 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                 tc_fence_before();
                 arrive_release(pfull(mi));
             }
+            // ---- the next run's Q, so that its S is under way during this run's result
+            const bool whole = run.whole(), valid_was = valid;
+            const int p_was = p, wb_was = wb, h_was = run.h, seq = run.who.x;
+            const int64_t orow_was = orow;
+            if (tile == 0 && !whole && threadIdx.x == 128)
+                a.split[blockIdx.x] = make_int4(run.bi, run.h, run.last_cta(), 0);
+            run.next();
+            find();
+            if (run.live()) load_q();
             // ---- this run's result
             wait_for(pvdone(mi), (sc - 1) & 1u, abort_flag, kErrEpilogue);
             tc_fence_after();
-            const bool whole = tile == 0 && len == u.tiles;
-            const int64_t unit = (int64_t)bi * pv.H + h;
-            if (tile == 0 && threadIdx.x == 128) {
-                // the CTA that holds tile x is the largest c with total * c / ncta <= x
-                const int64_t last = whole ? blockIdx.x : ((at + u.tiles - 1) * ncta + ncta - 1) / total;
-                a.span[unit] = make_int2(blockIdx.x, (int)last);
-            }
             constexpr int vc = FMT == FP8_E4M3 ? P::VC_E4M3 : P::VC_E5M2;
             const float fo = ex > -1000 ? pow2i(min(ex - vc, 127)) : 0.0f;
             const float r = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
@@ -869,11 +909,11 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                         if (tile_full<KT>(pv, u, j0)) continue;
 #pragma unroll 1
                         for (int j = j0; j < j0 + KT; ++j) {
-                            if (j > p || !(j >= wb || j < pv.sinks)) continue;
-                            const int s = pv.slot(who.x, j);
+                            if (j > p_was || !(j >= wb_was || j < pv.sinks)) continue;
+                            const int s = pv.slot(seq, j);
                             if (s < 0) continue;
-                            const float d = pv.vs[(int64_t)s * pv.H + h];
-                            const uint8_t *codes = pv.vc + (uint64_t)(uint32_t)s * (uint64_t)(pv.H * pv.Dh) + h * pv.Dh + c;
+                            const float d = pv.vs[(int64_t)s * pv.H + h_was];
+                            const uint8_t *codes = pv.vc + (uint64_t)(uint32_t)s * (uint64_t)(pv.H * pv.Dh) + h_was * pv.Dh + c;
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (c + i < pv.Dh) {
@@ -883,9 +923,9 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                         }
                     }
                 }
-                if (!valid || c >= pv.Dh) continue;
+                if (!valid_was || c >= pv.Dh) continue;
                 if (whole) {
-                    __nv_bfloat16 *op = a.out + orow * pv.Dh + c;
+                    __nv_bfloat16 *op = a.out + orow_was * pv.Dh + c;
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
                         if (c + i < pv.Dh) {
@@ -904,14 +944,13 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                 }
             }
             tc_fence_before();
-            if (valid) {
+            if (valid_was) {
                 if (whole) {
-                    if (a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : (mr + log2f(l)) * kLn2;
+                    if (a.lse) a.lse[orow_was] = l == 0.0f ? -INFINITY : (mr + log2f(l)) * kLn2;
                 } else {
                     *reinterpret_cast<float2 *>(part + (int64_t)ROWS * DH + 2 * (mi * 128 + row)) = make_float2(mr, l);
                 }
             }
-            advance(len);
         }
     }
 
@@ -932,12 +971,11 @@ k_prefill_join(const PagedView pv, const PrefillArgs a) {
     constexpr int E = DH / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
-    const int64_t bi = blockIdx.x / pv.H;
-    const int h = (int)(blockIdx.x % pv.H);
-    if (bi >= a.hdr[1]) return;
-    const int2 span = a.span[blockIdx.x];
-    if (span.x == span.y) return;
-    const int2 who = a.block[bi];
+    const int first = blockIdx.x;             // the CTA that began the unit, with the second of its parts
+    const int4 sp = a.split[first];
+    if (sp.x < 0) return;
+    const int2 who = a.block[sp.x];
+    const int h = sp.y, last = sp.z;
     const Unit u = unit_of<P::ROWS, P::KT>(pv, a, who.x, who.y);
     const int64_t stride = (int64_t)P::ROWS * (DH + 2);
     for (int row = blockIdx.y * 8 + warp; row < u.rho1 - u.rho0; row += gridDim.y * 8) {
@@ -947,8 +985,8 @@ k_prefill_join(const PagedView pv, const PrefillArgs a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.0f;
 #pragma unroll 4
-        for (int c = span.x; c <= span.y; ++c) {
-            const float *p = a.part + (2 * (int64_t)c + (c == span.x ? 1 : 0)) * stride;
+        for (int c = first; c <= last; ++c) {
+            const float *p = a.part + (2 * (int64_t)c + (c == first ? 1 : 0)) * stride;
             const float2 v = *reinterpret_cast<const float2 *>(p + (int64_t)P::ROWS * DH + 2 * row);
             const float nm = fmaxf(mx, v.x), al = exp2_fast(mx - nm), be = exp2_fast(v.x - nm);
             mx = nm;
@@ -973,8 +1011,8 @@ namespace {
 
 struct PrefillPlan {
     int DH, ctas;
-    int64_t units;            // at most, over all heads
-    size_t part, span, hdr, first, block, start, total;
+    int64_t blocks;           // row blocks, at most
+    size_t part, split, hdr, first, block, start, total;
 };
 
 PrefillPlan prefill_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t Dh, int sms) {
@@ -983,7 +1021,7 @@ PrefillPlan prefill_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t Dh
     p.DH = Dh <= 64 ? 64 : Dh <= 128 ? 128 : 256;
     p.ctas = sms;
     const int64_t rows = p.DH <= 128 ? 256 : 128, blocks = T * G / rows + std::min(B, T);
-    p.units = blocks * H;
+    p.blocks = blocks;
     size_t at = 0;
     auto take = [&at](size_t n) {
         const size_t was = at;
@@ -991,9 +1029,9 @@ PrefillPlan prefill_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t Dh
         return was;
     };
     p.part = take((size_t)p.ctas * 2 * rows * (p.DH + 2) * 4);
-    p.span = take((size_t)p.units * 8);
+    p.split = take((size_t)p.ctas * 16);
     p.hdr = take(16);
-    p.first = take((size_t)(B + 1) * 8);
+    p.first = take((size_t)B * 8);
     p.block = take((size_t)blocks * 8);
     p.start = take((size_t)p.ctas * 16);
     p.total = at;
@@ -1022,8 +1060,7 @@ cudaError_t launch_prefill(const PagedView &pv, const PrefillArgs &a, const Pref
     if (e != cudaSuccess) return e;
     e = pdl_launch(k_prefill<FMT, DH>, dim3(p.ctas), dim3(kThreads), P::SMEM, s, pv, a);
     if (e != cudaSuccess) return e;
-    const unsigned slices = (unsigned)std::max<int64_t>(1, std::min<int64_t>(16, 2048 / p.units));
-    return pdl_launch(k_prefill_join<DH>, dim3((unsigned)p.units, slices), dim3(256), 0, s, pv, a);
+    return pdl_launch(k_prefill_join<DH>, dim3(p.ctas, 8), dim3(256), 0, s, pv, a);
 }
 
 }  // namespace
@@ -1067,12 +1104,12 @@ extern "C" fp8_status fp8_paged_attention_prefill(
     a.B = (int)B;
     a.G = (int)(Hq / H);
     a.ctas = p.ctas;
-    a.max_blocks = p.units / H;
+    a.max_blocks = p.blocks;
     a.scale = softmax_scale;
     a.out = (__nv_bfloat16 *)out_bf16;
     a.lse = lse;
     a.part = (float *)(ws + p.part);
-    a.span = (int2 *)(ws + p.span);
+    a.split = (int4 *)(ws + p.split);
     a.hdr = (int64_t *)(ws + p.hdr);
     a.first_block = (int64_t *)(ws + p.first);
     a.block = (int2 *)(ws + p.block);
