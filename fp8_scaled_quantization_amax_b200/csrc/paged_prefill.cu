@@ -18,11 +18,11 @@
 // maximum of a tile is looked for nor O rescaled but seldom, and weights are
 // exact to 2^-11 down to 2^-21 of the largest in fp16.
 //
-// Warp roles: warp 0 issues the MMAs; warps 1 to 3 look up the tiles' pages and
-// scales; warpgroups 1 and 2 are the softmax of the
-// two row tiles (and load Q, rescale O, write results); warpgroup 3 reads the
-// cache through the block table, converts and writes the K and V tiles (two
-// buffers each).  The tensor core alternates between the row tiles, so one
+// Warp roles: warp 0 issues the MMAs; warps 2 and 3 look up the tiles' slots and
+// scales, warp 1 copies their codes (TMA boxes of 8 rows or more of one head where
+// the page size allows it, cp.async otherwise); warpgroup 3 converts them to the
+// fp16 tiles; warpgroups 1 and 2 are the softmax of the two row tiles (and load
+// Q, rescale O, write results).  The tensor core alternates between the row tiles, so one
 // tile's softmax runs under the other's products.
 //
 // Split: k_prefill_plan lists the row blocks of all sequences and deals the
@@ -56,7 +56,7 @@ struct PrefillArgs {
     int64_t ld_q;
     const int64_t *q_off;
     int64_t T;
-    int B, G, ctas;
+    int B, G, ctas, box;
     int64_t max_blocks;       // row blocks that the workspace has room for
     float scale;
     __nv_bfloat16 *out;
@@ -74,15 +74,17 @@ struct Pre {
     static constexpr int MT = DH <= 128 ? 2 : 1;          // 128-row tiles of a unit
     static constexpr int KT = DH <= 128 ? 128 : 64;       // positions per tile
     static constexpr int ROWS = 128 * MT;
-    static constexpr int QB = 128 * DH * 2, KVB = KT * DH * 2;   // bytes of a Q tile, of a K or V buffer
+    static constexpr int QB = 128 * DH * 2, KVB = KT * DH * 2;   // bytes of a Q tile, of a K or V tile in fp16
+    static constexpr int RAW = KT * DH;                   // and in codes
+    static constexpr int RING = 3;                        // buffers of each kind: K, V, K, V, ... in turn
     static constexpr int META = 8;                        // tiles whose scales and masks are kept
-    static constexpr int OFF_K = MT * QB, OFF_V = OFF_K + 2 * KVB, OFF_M = OFF_V + 2 * KVB;
+    static constexpr int OFF_KV = MT * QB, OFF_RAW = OFF_KV + RING * KVB, OFF_M = OFF_RAW + RING * RAW;
     static constexpr int M_DK = 0, M_DV = KT * 4, M_SLOT = KT * 8, M_LIVE = KT * 12, M_MAX = M_LIVE + 16,
                          M_EXP = M_MAX + 16, M_BYTES = M_EXP + 16;
-    static constexpr int OFF_F = OFF_M + META * M_BYTES;   // column factors: [row tile][2][KT]
+    static constexpr int OFF_F = OFF_M + META * M_BYTES;  // column factors: [row tile][2][KT]
     static constexpr int OFF_BAR = OFF_F + MT * 2 * KT * 4;
-    static constexpr int NBARS = 8 + 4 * MT + 1 + META;
-    static constexpr size_t SMEM = 1024 + OFF_BAR + NBARS * 8 + 64;
+    static constexpr int NBARS = 4 * RING + 4 * MT + 1 + META;
+    static constexpr size_t SMEM = 1024 + OFF_BAR + NBARS * 8;
     static constexpr int S_COL = KT, O_COL = 256;         // TMEM: S of tile i at i * S_COL, O at O_COL + i * DH
     static constexpr int VC_E4M3 = 6, VC_E5M2 = -1;       // code * scale * 2^(VC - exponent of the largest) < 2^16
 };
@@ -395,6 +397,13 @@ __device__ __forceinline__ void st_shared_u32(uint32_t a, uint32_t v) {
 __device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Low and high words of the shared-memory descriptors, 128-byte swizzle.  K-major
 // (Q, K): rows of 64 elements, 8 rows 1 KiB apart.  MN-major (V: a row per
@@ -412,9 +421,11 @@ __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn) {
 __device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u; }
 
 // ----------------------------------------------------------------- kernel --
-template <int FMT, int DH>
+// TMA: boxes of a.box rows, which divides the page size; otherwise cp.async.
+template <int FMT, int DH, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1)
-k_prefill(const PagedView pv, const PrefillArgs a) {
+k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedView pv,
+          const PrefillArgs a) {
     using P = Pre<DH>;
     constexpr int MT = P::MT, KT = P::KT, ROWS = P::ROWS;
     extern __shared__ uint8_t smem_raw[];
@@ -425,23 +436,25 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
     const uint32_t sb = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
     const uint32_t bar0 = sb + P::OFF_BAR;
-    auto kfull = [&](int i) { return bar0 + 8 * i; };
-    auto kempty = [&](int i) { return bar0 + 8 * (2 + i); };
-    auto vfull = [&](int i) { return bar0 + 8 * (4 + i); };
-    auto vempty = [&](int i) { return bar0 + 8 * (6 + i); };
-    auto qfull = [&](int i) { return bar0 + 8 * (8 + i); };
-    auto sfull = [&](int i) { return bar0 + 8 * (8 + MT + i); };
-    auto pfull = [&](int i) { return bar0 + 8 * (8 + 2 * MT + i); };
-    auto pvdone = [&](int i) { return bar0 + 8 * (8 + 3 * MT + i); };
-    const uint32_t drain = bar0 + 8 * (8 + 4 * MT);
-    auto mfull = [&](uint32_t k) { return bar0 + 8 * (9 + 4 * MT + k % P::META); };
+    constexpr int RING = P::RING;
+    auto rfull = [&](uint32_t i) { return bar0 + 8 * (i % RING); };              // codes of unit i = 2 tile + (V ? 1 : 0)
+    auto rempty = [&](uint32_t i) { return bar0 + 8 * (RING + i % RING); };
+    auto ffull = [&](uint32_t i) { return bar0 + 8 * (2 * RING + i % RING); };   // the same in fp16
+    auto fempty = [&](uint32_t i) { return bar0 + 8 * (3 * RING + i % RING); };
+    auto phase = [](uint32_t i) { return (i / RING) & 1u; };
+    auto qfull = [&](int i) { return bar0 + 8 * (4 * RING + i); };
+    auto sfull = [&](int i) { return bar0 + 8 * (4 * RING + MT + i); };
+    auto pfull = [&](int i) { return bar0 + 8 * (4 * RING + 2 * MT + i); };
+    auto pvdone = [&](int i) { return bar0 + 8 * (4 * RING + 3 * MT + i); };
+    const uint32_t drain = bar0 + 8 * (4 * RING + 4 * MT);
+    auto mfull = [&](uint32_t k) { return bar0 + 8 * (4 * RING + 4 * MT + 1 + k % P::META); };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(kfull(i), 128);
-            mbar_init(vfull(i), 128);
-            mbar_init(kempty(i), 1);
-            mbar_init(vempty(i), 1);
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(rfull(i), TMA ? 1 : 32);
+            mbar_init(rempty(i), 128);
+            mbar_init(ffull(i), 128);
+            mbar_init(fempty(i), 1);
         }
         for (int i = 0; i < MT; ++i) {
             mbar_init(qfull(i), 128);
@@ -478,7 +491,7 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
             uint32_t kc = 0, pc[2] = {0, 0}, qc[2] = {0, 0};   // tiles so far; P tiles; runs
             bool ok = true;
             auto issue_s = [&](int i, uint32_t buf) {
-                const uint32_t qa = sb + i * P::QB, ka = sb + P::OFF_K + buf * P::KVB;
+                const uint32_t qa = sb + i * P::QB, ka = sb + P::OFF_KV + buf * P::KVB;
 #pragma unroll
                 for (int blk = 0; blk < DH / 64; ++blk) {
                     const uint32_t qd = desc_lo(qa + blk * 128 * 128, 0), kd = desc_lo(ka + blk * KT * 128, 0);
@@ -492,51 +505,94 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
             for (; ok && run.live(); run.next()) {
                 const int len = run.len, tiles_m = run.u.rho1 - run.u.rho0 > 128 ? MT : 1;
                 for (int i = 0; ok && i < tiles_m; ++i) ok = wait_for(qfull(i), qc[i]++ & 1u, abort_flag, kErrMma);
-                ok = ok && wait_for(kfull(kc & 1), (kc >> 1) & 1u, abort_flag, kErrMma);
+                ok = ok && wait_for(ffull(2 * kc), phase(2 * kc), abort_flag, kErrMma);
                 if (!ok) break;
                 tc_fence_after();
-                for (int i = 0; i < tiles_m; ++i) issue_s(i, kc & 1);
-                commit_one(kempty(kc & 1), leader);
+                for (int i = 0; i < tiles_m; ++i) issue_s(i, 2 * kc % RING);
+                commit_one(fempty(2 * kc), leader);
                 for (int k = 0; ok && k < len; ++k, ++kc) {
-                    ok = wait_for(vfull(kc & 1), (kc >> 1) & 1u, abort_flag, kErrMma);
+                    const uint32_t vi = 2 * kc + 1, ki = 2 * kc + 2;   // V of this tile, K of the next
+                    ok = wait_for(ffull(vi), phase(vi), abort_flag, kErrMma);
                     for (int i = 0; ok && i < tiles_m; ++i) {
                         ok = wait_for(pfull(i), pc[i]++ & 1u, abort_flag, kErrMma);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t vd = desc_lo(sb + P::OFF_V + (kc & 1) * P::KVB, KT * 128);
+                        const uint32_t vd = desc_lo(sb + P::OFF_KV + vi % RING * P::KVB, KT * 128);
 #pragma unroll
                         for (int s = 0; s < KT / 16; ++s)
                             mma_ts(tmem + P::O_COL + i * DH, tmem + i * P::S_COL + 8 * s, vd + 128 * s, kDescHi, id_o,
                                    (k | s) ? 1u : 0u, leader);
                         commit_one(pvdone(i), leader);
                         if (k + 1 < len) {
-                            if (i == 0) ok = wait_for(kfull((kc + 1) & 1), ((kc + 1) >> 1) & 1u, abort_flag, kErrMma);
+                            if (i == 0) ok = wait_for(ffull(ki), phase(ki), abort_flag, kErrMma);
                             if (!ok) break;
                             tc_fence_after();
-                            issue_s(i, (kc + 1) & 1);
+                            issue_s(i, ki % RING);
                         }
                     }
                     if (!ok) break;
-                    commit_one(vempty(kc & 1), leader);
-                    if (k + 1 < len) commit_one(kempty((kc + 1) & 1), leader);
+                    commit_one(fempty(vi), leader);
+                    if (k + 1 < len) commit_one(fempty(ki), leader);
                 }
             }
             commit_one(drain, leader);
             wait_bar_drain(drain, 0u);
             __syncwarp();
+        } else if (warp == 1) {
+            // -------------------------- codes of the tiles, K and V in turn --
+            uint32_t kc = 0;
+            for (; run.live(); run.next()) {
+                for (int k = 0; k < run.len; ++k, ++kc) {
+                    wait_for(mfull(kc), (kc / P::META) & 1u, abort_flag, kErrProducer);
+                    const uint32_t slots = sb + P::OFF_M + (kc % P::META) * P::M_BYTES + P::M_SLOT;
+                    for (uint32_t i = 2 * kc; i < 2 * kc + 2; ++i) {
+                        wait_for(rempty(i), phase(i) ^ 1u, abort_flag, kErrProducer);
+                        const uint32_t dst = sb + P::OFF_RAW + i % RING * P::RAW;
+                        if constexpr (TMA) {
+                            if (lane == 0) mbar_expect_tx(rfull(i), P::RAW);
+                            // lane l: the box at row l * box; one without a slot starts past the last: zeros
+                            const int r = lane * a.box;
+                            if (r < KT) {
+                                const int s = (int)ld_shared_u32(slots + 4 * r);
+                                const int z = s >= 0 ? s : (int)(pv.bs.d * (uint32_t)pv.num_blocks);
+                                tma_load_3d(dst + (uint32_t)r * DH, i & 1 ? &tmV : &tmK, rfull(i), 0, run.h, z);
+                            }
+                        } else {
+                            const uint8_t *codes = (i & 1 ? pv.vc : pv.kc) + run.h * pv.Dh;
+                            constexpr int CH = DH / 16;
+                            for (int x = lane; x < KT * CH; x += 32) {
+                                const int s = (int)ld_shared_u32(slots + 4 * (x / CH)), c = x % CH;
+                                const int n = s >= 0 && 16 * c < pv.Dh ? 16 : 0;
+                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * x),
+                                             "l"(codes + (uint64_t)(uint32_t)max(s, 0) * (uint32_t)(pv.H * pv.Dh) +
+                                                 (n ? 16 * c : 0)),
+                                             "r"(n)
+                                             : "memory");
+                            }
+                            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(rfull(i)) : "memory");
+                        }
+                    }
+                }
+            }
+            if constexpr (!TMA) asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
         } else {
             // ------------------------- slots, scales and masks of tiles ---
-            // Warps 1 to 3 take turns, a few tiles ahead of the converter: a tile's look-up is two dependent
-            // loads, which nothing there could hide.
+            // Warps 2 and 3 take turns, a few tiles ahead: a tile's look-up is two dependent loads, which nothing
+            // behind it could hide.
             uint32_t kc = 0;
             for (; run.live(); run.next()) {
                 const Unit &u = run.u;
                 const int h = run.h;
                 for (int k = 0; k < run.len; ++k, ++kc) {
                     // S of tile kc - 5 is issued behind the softmax of tile kc - 6: nobody reads kc - 8 any more.
-                    // Every warp waits for every tile: a parity only tells a phase from its neighbours.
-                    if (kc >= 5) wait_for(kempty((kc - 5) & 1), ((kc - 5) >> 1) & 1u, abort_flag, kErrProducer);
-                    if (kc % 3 != (uint32_t)(warp - 1)) continue;
+                    // Both warps wait for every buffer: a parity only tells a phase from its neighbours.
+                    if (kc >= 5) {
+                        const uint32_t i = 2 * (kc - 5);
+                        if (i > 0) wait_for(fempty(i - 1), phase(i - 1), abort_flag, kErrProducer);
+                        wait_for(fempty(i), phase(i), abort_flag, kErrProducer);
+                    }
+                    if ((kc & 1) != (uint32_t)(warp & 1)) continue;
                     uint8_t *m = smem + P::OFF_M + (kc % P::META) * P::M_BYTES;
                     const int j0 = tile_pos<KT>(u, run.tile + k);
                     int s[KT / 32];
@@ -573,10 +629,8 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
         // ------------------------------------------- K and V converter ----
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
         constexpr int CH = DH / 16, RPI = 32 / CH, ITS = KT / (4 * RPI);   // 16-code chunks of a row; rows per load
-        const int tid = threadIdx.x - 384, w = tid >> 5, c = lane % CH, r0 = w * RPI + lane / CH;
+        const int tid = threadIdx.x - 384, c = lane % CH, r0 = (tid >> 5) * RPI + lane / CH;
         const int swap = (c >> 2) & 1;        // half the chunks are stored high half first: no bank conflicts
-        const bool c_live = 16 * c < pv.Dh;
-        const uint32_t row_bytes = (uint32_t)(pv.H * pv.Dh);
         uint32_t kc = 0;
         int ex = -1000;                       // exponent of the largest V scale of the run so far
         auto meta = [&](uint32_t k) -> uint32_t { return sb + P::OFF_M + (k % P::META) * P::M_BYTES; };
@@ -590,16 +644,16 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
             if (mx) ex = max(ex, max((int)(mx >> 23) - 127, -100));
             if (tid == 0) st_shared_u32(meta(k) + P::M_EXP, (uint32_t)ex);
         };
-        auto load = [&](uint4 (&v)[ITS], const uint8_t *codes, uint32_t k) {
-            const uint32_t slots = meta(k) + P::M_SLOT + 4 * r0;
-            codes += run.h * pv.Dh + 16 * c;
+        // this thread's chunks of unit i, and the buffer back
+        auto load = [&](uint4 (&v)[ITS], uint32_t i) {
+            wait_for(rfull(i), phase(i), abort_flag, kErrProducer);
+            const uint32_t src = sb + P::OFF_RAW + i % RING * P::RAW + r0 * DH + 16 * c;
 #pragma unroll
-            for (int i = 0; i < ITS; ++i) {
-                const int s = (int)ld_shared_u32(slots + i * 16 * RPI);
-                v[i] = make_uint4(0, 0, 0, 0);
-                if (s >= 0 && c_live)
-                    v[i] = *reinterpret_cast<const uint4 *>(codes + (uint64_t)(uint32_t)s * row_bytes);
+            for (int e = 0; e < ITS; ++e) {
+                const float4 f = ld_shared_f4(src + e * 4 * RPI * DH);
+                v[e] = make_uint4(__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z), __float_as_uint(f.w));
             }
+            arrive_release(rempty(i));
         };
         auto put = [&](uint32_t base, int row, const uint32_t (&x)[8]) {
             const uint32_t at_row = base + (c >> 2) * (KT * 128) + row * 128, ch = (c & 3) * 2;
@@ -611,77 +665,72 @@ k_prefill(const PagedView pv, const PrefillArgs a) {
                 else st_shared16(dst, x[0], x[1], x[2], x[3]);
             }
         };
-        uint4 kv[ITS], vv[ITS];
-        if (run.live()) {
-            look_up(0, true);
-            load(kv, pv.kc, 0);
-            load(vv, pv.vc, 0);
-        }
-        int k = 0;                            // tile of the run
-        for (; run.live(); ++kc) {
-            {
-                const uint32_t buf = kc & 1, par = ((kc >> 1) & 1u) ^ 1u;
-                const bool full = tile_full<KT>(pv, run.u, tile_pos<KT>(run.u, run.tile + k));
-                const int my_ex = ex;
-                const uint32_t dv = meta(kc) + P::M_DV + 4 * r0;
+        for (; run.live(); run.next()) {
+            for (int k = 0; k < run.len; ++k, ++kc) {
+                look_up(kc, k == 0);
+                uint4 q[ITS];
                 // ---- K
-                wait_for(kempty(buf), par, abort_flag, kErrProducer);
-                const uint32_t kb = sb + P::OFF_K + buf * P::KVB;
+                uint32_t i = 2 * kc;
+                load(q, i);
+                wait_for(fempty(i), phase(i) ^ 1u, abort_flag, kErrProducer);
+                uint32_t dst = sb + P::OFF_KV + i % RING * P::KVB;
 #pragma unroll
-                for (int i = 0; i < ITS; ++i) {
+                for (int e = 0; e < ITS; ++e) {
                     uint32_t x[8];
-                    to_f16x4<FMT>(kv[i].x, x[0], x[1]);
-                    to_f16x4<FMT>(kv[i].y, x[2], x[3]);
-                    to_f16x4<FMT>(kv[i].z, x[4], x[5]);
-                    to_f16x4<FMT>(kv[i].w, x[6], x[7]);
-                    put(kb, i * 4 * RPI + r0, x);
+                    to_f16x4<FMT>(q[e].x, x[0], x[1]);
+                    to_f16x4<FMT>(q[e].y, x[2], x[3]);
+                    to_f16x4<FMT>(q[e].z, x[4], x[5]);
+                    to_f16x4<FMT>(q[e].w, x[6], x[7]);
+                    put(dst, e * 4 * RPI + r0, x);
                 }
                 fence_async();
-                arrive_release(kfull(buf));
-                // ---- the next tile's slots, and its K on the way while V is converted
-                const bool fresh = k + 1 == run.len;
-                if (fresh) run.next();
-                k = fresh ? 0 : k + 1;
-                const bool more = run.live();
-                if (more) look_up(kc + 1, fresh);
-                if (more) load(kv, pv.kc, kc + 1);
+                arrive_release(ffull(i));
                 // ---- V, scaled
-                wait_for(vempty(buf), par, abort_flag, kErrProducer);
-                const uint32_t vb = sb + P::OFF_V + buf * P::KVB;
-                const float fp = my_ex > -1000 ? pow2i(max((FMT == FP8_E4M3 ? P::VC_E4M3 : P::VC_E5M2) - my_ex, -126)) : 0.0f;
-                uint32_t bad = 0;
+                ++i;
+                load(q, i);
+                const uint32_t dv = meta(kc) + P::M_DV + 4 * r0;
+                const float fp = ex > -1000 ? pow2i(max((FMT == FP8_E4M3 ? P::VC_E4M3 : P::VC_E5M2) - ex, -126)) : 0.0f;
+                float f[ITS];
 #pragma unroll
-                for (int i = 0; i < ITS; ++i) {
-                    const int row = i * 4 * RPI + r0;
-                    float f = __uint_as_float(ld_shared_u32(dv + i * 16 * RPI)) * fp;
-                    uint4 q = vv[i];
-                    if (!full) {              // what only some rows see must be finite
-                        const uint32_t nf = nonfinite4<FMT>(q.x) | nonfinite4<FMT>(q.y) | nonfinite4<FMT>(q.z) |
-                                            nonfinite4<FMT>(q.w);
-                        if (nf | !(fabsf(f) < INFINITY)) {
+                for (int e = 0; e < ITS; ++e) f[e] = __uint_as_float(ld_shared_u32(dv + e * 16 * RPI)) * fp;
+                uint32_t all = 0xFFFFFFFFu;
+#pragma unroll
+                for (int e = 0; e < KT / 32; ++e) all &= ld_shared_u32(meta(kc) + P::M_LIVE + 4 * e);
+                if (all != 0xFFFFFFFFu || !tile_full<KT>(pv, run.u, tile_pos<KT>(run.u, run.tile + k))) {
+                    // slots that are no live position are zeros, and what only some rows see must be finite
+                    uint32_t bad = 0;
+#pragma unroll
+                    for (int e = 0; e < ITS; ++e) {
+                        const int r = e * 4 * RPI + r0;
+                        const bool live = (ld_shared_u32(meta(kc) + P::M_LIVE + 4 * (r >> 5)) >> (r & 31)) & 1u;
+                        if (!live) q[e] = make_uint4(0, 0, 0, 0);
+                        const uint32_t nf = nonfinite4<FMT>(q[e].x) | nonfinite4<FMT>(q[e].y) |
+                                            nonfinite4<FMT>(q[e].z) | nonfinite4<FMT>(q[e].w);
+                        if (nf || !(fabsf(f[e]) < INFINITY)) {
                             bad = 1;
-                            auto clean = [](uint32_t x) {
-                                const uint32_t b = nonfinite4<FMT>(x);
-                                return x & ~((b >> 7) * 0xFFu);
-                            };
-                            q = make_uint4(clean(q.x), clean(q.y), clean(q.z), clean(q.w));
-                            if (!(fabsf(f) < INFINITY)) f = 0.0f;
+                            auto clean = [](uint32_t x) { return x & ~((nonfinite4<FMT>(x) >> 7) * 0xFFu); };
+                            q[e] = make_uint4(clean(q[e].x), clean(q[e].y), clean(q[e].z), clean(q[e].w));
+                            if (!(fabsf(f[e]) < INFINITY)) f[e] = 0.0f;
                         }
                     }
-                    const uint32_t f2 = pack_f16x2(f, f);
-                    uint32_t x[8];
-                    to_f16x4<FMT>(q.x, x[0], x[1]);
-                    to_f16x4<FMT>(q.y, x[2], x[3]);
-                    to_f16x4<FMT>(q.z, x[4], x[5]);
-                    to_f16x4<FMT>(q.w, x[6], x[7]);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = mul_f16x2(x[e], f2);
-                    put(vb, row, x);
+                    if (bad) s_poison = 1u;
                 }
-                if (bad) s_poison = 1u;
+                wait_for(fempty(i), phase(i) ^ 1u, abort_flag, kErrProducer);
+                dst = sb + P::OFF_KV + i % RING * P::KVB;
+#pragma unroll
+                for (int e = 0; e < ITS; ++e) {
+                    const uint32_t f2 = pack_f16x2(f[e], f[e]);
+                    uint32_t x[8];
+                    to_f16x4<FMT>(q[e].x, x[0], x[1]);
+                    to_f16x4<FMT>(q[e].y, x[2], x[3]);
+                    to_f16x4<FMT>(q[e].z, x[4], x[5]);
+                    to_f16x4<FMT>(q[e].w, x[6], x[7]);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) x[y] = mul_f16x2(x[y], f2);
+                    put(dst, e * 4 * RPI + r0, x);
+                }
                 fence_async();
-                arrive_release(vfull(buf));
-                if (more) load(vv, pv.vc, kc + 1);
+                arrive_release(ffull(i));
             }
         }
     } else if (wg - 1 < MT) {
@@ -1038,8 +1087,22 @@ PrefillPlan prefill_plan(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t Dh
     return p;
 }
 
-template <int FMT, int DH>
-cudaError_t launch_prefill(const PagedView &pv, const PrefillArgs &a, const PrefillPlan &p, cudaStream_t s) {
+// 3-D map over codes [slots, H, Dh]: boxes of `rows` slots of one head, DH bytes
+// wide (a smaller head reads zeros behind its end).
+bool make_map_tiles(CUtensorMap *map, const void *codes, const PagedView &pv, int DH, int rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)pv.Dh, (cuuint64_t)pv.H, (cuuint64_t)pv.bs.d * (cuuint64_t)pv.num_blocks};
+    cuuint64_t strides[2] = {(cuuint64_t)pv.Dh, (cuuint64_t)pv.Dh * (cuuint64_t)pv.H};
+    cuuint32_t box[3] = {(cuuint32_t)DH, 1, (cuuint32_t)rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(codes), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT, int DH, bool TMA>
+cudaError_t launch_main(const PagedView &pv, const PrefillArgs &a, const PrefillPlan &p, cudaStream_t s) {
     using P = Pre<DH>;
     // shared memory and the register split are checked once per device
     static std::atomic<uint64_t> ready{0};
@@ -1049,16 +1112,28 @@ cudaError_t launch_prefill(const PagedView &pv, const PrefillArgs &a, const Pref
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_acquire) & bit)) {
         cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, k_prefill<FMT, DH>);
+        e = cudaFuncGetAttributes(&fa, k_prefill<FMT, DH, TMA>);
         if (e != cudaSuccess) return e;
         if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;   // setmaxnreg needs exactly these
-        e = cudaFuncSetAttribute(k_prefill<FMT, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::SMEM);
+        e = cudaFuncSetAttribute(k_prefill<FMT, DH, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::SMEM);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
+    CUtensorMap tk = {}, tv = {};
+    if (TMA && (!make_map_tiles(&tk, pv.kc, pv, DH, a.box) || !make_map_tiles(&tv, pv.vc, pv, DH, a.box)))
+        return cudaErrorInvalidValue;
+    return pdl_launch(k_prefill<FMT, DH, TMA>, dim3(p.ctas), dim3(kThreads), P::SMEM, s, tk, tv, pv, a);
+}
+
+template <int FMT, int DH>
+cudaError_t launch_prefill(const PagedView &pv, const PrefillArgs &a, const PrefillPlan &p, cudaStream_t s) {
+    using P = Pre<DH>;
+    cudaError_t e;
     e = pdl_launch(k_prefill_plan<P::ROWS, P::KT>, dim3(1), dim3(kPlanThreads), 0, s, pv, a);
     if (e != cudaSuccess) return e;
-    e = pdl_launch(k_prefill<FMT, DH>, dim3(p.ctas), dim3(kThreads), P::SMEM, s, pv, a);
+    // pages that 8 rows do not divide, and a pool without pages, have no boxes
+    e = pv.bs.d % 8 == 0 && pv.num_blocks > 0 ? launch_main<FMT, DH, true>(pv, a, p, s)
+                                              : launch_main<FMT, DH, false>(pv, a, p, s);
     if (e != cudaSuccess) return e;
     return pdl_launch(k_prefill_join<DH>, dim3(p.ctas, 8), dim3(256), 0, s, pv, a);
 }
@@ -1105,6 +1180,7 @@ extern "C" fp8_status fp8_paged_attention_prefill(
     a.G = (int)(Hq / H);
     a.ctas = p.ctas;
     a.max_blocks = p.blocks;
+    a.box = block_size % 32 == 0 ? 32 : block_size % 16 == 0 ? 16 : 8;
     a.scale = softmax_scale;
     a.out = (__nv_bfloat16 *)out_bf16;
     a.lse = lse;
