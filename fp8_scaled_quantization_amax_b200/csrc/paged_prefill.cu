@@ -57,6 +57,7 @@ struct PrefillArgs {
     const int64_t *q_off;
     int64_t T;
     int B, G, ctas, box;
+    FastDiv gdiv;             // by G
     int64_t max_blocks;       // row blocks that the workspace has room for
     float scale;
     __nv_bfloat16 *out;
@@ -81,8 +82,7 @@ struct Pre {
     static constexpr int OFF_KV = MT * QB, OFF_RAW = OFF_KV + RING * KVB, OFF_M = OFF_RAW + RING * RAW;
     static constexpr int M_DK = 0, M_DV = KT * 4, M_SLOT = KT * 8, M_LIVE = KT * 12, M_MAX = M_LIVE + 16,
                          M_EXP = M_MAX + 16, M_BYTES = M_EXP + 16;
-    static constexpr int OFF_F = OFF_M + META * M_BYTES;  // column factors: [row tile][2][KT]
-    static constexpr int OFF_BAR = OFF_F + MT * 2 * KT * 4;
+    static constexpr int OFF_BAR = OFF_M + META * M_BYTES;
     static constexpr int NBARS = 4 * RING + 4 * MT + 1 + META;
     static constexpr size_t SMEM = 1024 + OFF_BAR + NBARS * 8;
     static constexpr int S_COL = KT, O_COL = 256;         // TMEM: S of tile i at i * S_COL, O at O_COL + i * DH
@@ -112,8 +112,8 @@ __device__ __forceinline__ Unit unit_of(const PagedView &pv, const PrefillArgs &
     u.rho0 = mb * ROWS;
     u.rho1 = min(u.rho0 + ROWS, u.count * a.G);
     const int p0 = u.n - u.count;
-    u.pmin = p0 + u.rho0 / a.G;
-    u.pmax = p0 + (u.rho1 - 1) / a.G;
+    u.pmin = p0 + (int)a.gdiv.div((uint32_t)u.rho0);
+    u.pmax = p0 + (int)a.gdiv.div((uint32_t)(u.rho1 - 1));
     if (u.pmax < 0) {                 // no row sees anything: one tile, all masked
         u.first_tile = u.sink_tiles = 0;
         u.tiles = 1;
@@ -136,7 +136,7 @@ __device__ __forceinline__ bool tile_full(const PagedView &pv, const Unit &u, in
 
 // A unit costs its tiles and this many more, for Q and the results.  Laid end to
 // end in cost, a unit's first kUnitCost places hold no tile.
-constexpr int kUnitCost = 3;
+constexpr int kUnitCost = 6;
 
 constexpr int kPlanThreads = 1024;
 __device__ int64_t plan_scan(int64_t v, int64_t *buf, int64_t *total) {   // exclusive, block-wide
@@ -334,7 +334,7 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // waits for the loads in flight; the registers of this array cannot be read above it
 template <int N>
 __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[N]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;");
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
@@ -432,6 +432,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // s_poison: something was taken out of V (for good: later results of this CTA look again for nothing)
     __shared__ uint32_t s_tmem, s_abort, s_poison, s_qmax[MT][4];
+    __shared__ float4 s_factor[MT][2][KT / 4];   // column factors of a row tile's softmax, two tiles
     volatile uint32_t *abort_flag = &s_abort;
     const uint32_t sb = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
@@ -490,48 +491,47 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             constexpr uint32_t id_s = idesc_f16(128, KT, false), id_o = idesc_f16(128, DH, true);
             uint32_t kc = 0, pc[2] = {0, 0}, qc[2] = {0, 0};   // tiles so far; P tiles; runs
             bool ok = true;
-            auto issue_s = [&](int i, uint32_t buf) {
-                const uint32_t qa = sb + i * P::QB, ka = sb + P::OFF_KV + buf * P::KVB;
-#pragma unroll
-                for (int blk = 0; blk < DH / 64; ++blk) {
-                    const uint32_t qd = desc_lo(qa + blk * 128 * 128, 0), kd = desc_lo(ka + blk * KT * 128, 0);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        mma_ss(tmem + i * P::S_COL, qd + 2 * s, kDescHi, kd + 2 * s, kDescHi, id_s, (blk | s) ? 1u : 0u,
-                               leader);
-                }
-                commit_one(sfull(i), leader);
-            };
             for (; ok && run.live(); run.next()) {
                 const int len = run.len, tiles_m = run.u.rho1 - run.u.rho0 > 128 ? MT : 1;
-                for (int i = 0; ok && i < tiles_m; ++i) ok = wait_for(qfull(i), qc[i]++ & 1u, abort_flag, kErrMma);
-                ok = ok && wait_for(ffull(2 * kc), phase(2 * kc), abort_flag, kErrMma);
-                if (!ok) break;
-                tc_fence_after();
-                for (int i = 0; i < tiles_m; ++i) issue_s(i, 2 * kc % RING);
-                commit_one(fempty(2 * kc), leader);
-                for (int k = 0; ok && k < len; ++k, ++kc) {
-                    const uint32_t vi = 2 * kc + 1, ki = 2 * kc + 2;   // V of this tile, K of the next
-                    ok = wait_for(ffull(vi), phase(vi), abort_flag, kErrMma);
+                // Step k: P V of tile k, then S of tile k + 1, for each row tile.  The loops stay rolled: four roles
+                // share an instruction cache.
+#pragma unroll 1
+                for (int k = -1; ok && k < len; ++k) {
+                    const uint32_t vi = 2 * kc + 1, ki = k < 0 ? 2 * kc : 2 * kc + 2;   // V of tile k, K of tile k + 1
+                    if (k >= 0) ok = wait_for(ffull(vi), phase(vi), abort_flag, kErrMma);
+                    else for (int i = 0; ok && i < tiles_m; ++i) ok = wait_for(qfull(i), qc[i]++ & 1u, abort_flag, kErrMma);
+#pragma unroll 1
                     for (int i = 0; ok && i < tiles_m; ++i) {
-                        ok = wait_for(pfull(i), pc[i]++ & 1u, abort_flag, kErrMma);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t vd = desc_lo(sb + P::OFF_KV + vi % RING * P::KVB, KT * 128);
-#pragma unroll
-                        for (int s = 0; s < KT / 16; ++s)
-                            mma_ts(tmem + P::O_COL + i * DH, tmem + i * P::S_COL + 8 * s, vd + 128 * s, kDescHi, id_o,
-                                   (k | s) ? 1u : 0u, leader);
-                        commit_one(pvdone(i), leader);
+                        if (k >= 0) {
+                            const uint32_t par = (i ? pc[1]++ : pc[0]++) & 1u;
+                            ok = wait_for(pfull(i), par, abort_flag, kErrMma);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t vd = desc_lo(sb + P::OFF_KV + vi % RING * P::KVB, KT * 128);
+#pragma unroll 2
+                            for (int s = 0; s < KT / 16; ++s)
+                                mma_ts(tmem + P::O_COL + i * DH, tmem + i * P::S_COL + 8 * s, vd + 128 * s, kDescHi, id_o,
+                                       (k | s) ? 1u : 0u, leader);
+                            commit_one(pvdone(i), leader);
+                        }
                         if (k + 1 < len) {
                             if (i == 0) ok = wait_for(ffull(ki), phase(ki), abort_flag, kErrMma);
                             if (!ok) break;
                             tc_fence_after();
-                            issue_s(i, ki % RING);
+                            const uint32_t qd = desc_lo(sb + i * P::QB, 0);
+                            const uint32_t kd = desc_lo(sb + P::OFF_KV + ki % RING * P::KVB, 0);
+#pragma unroll 2
+                            for (int s = 0; s < DH / 16; ++s)       // 64 elements to a swizzled block
+                                mma_ss(tmem + i * P::S_COL, qd + (s >> 2) * (128 * 128 >> 4) + 2 * (s & 3), kDescHi,
+                                       kd + (s >> 2) * (KT * 128 >> 4) + 2 * (s & 3), kDescHi, id_s, s ? 1u : 0u, leader);
+                            commit_one(sfull(i), leader);
                         }
                     }
                     if (!ok) break;
-                    commit_one(fempty(vi), leader);
+                    if (k >= 0) {
+                        commit_one(fempty(vi), leader);
+                        ++kc;
+                    }
                     if (k + 1 < len) commit_one(fempty(ki), leader);
                 }
             }
@@ -644,17 +644,6 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             if (mx) ex = max(ex, max((int)(mx >> 23) - 127, -100));
             if (tid == 0) st_shared_u32(meta(k) + P::M_EXP, (uint32_t)ex);
         };
-        // this thread's chunks of unit i, and the buffer back
-        auto load = [&](uint4 (&v)[ITS], uint32_t i) {
-            wait_for(rfull(i), phase(i), abort_flag, kErrProducer);
-            const uint32_t src = sb + P::OFF_RAW + i % RING * P::RAW + r0 * DH + 16 * c;
-#pragma unroll
-            for (int e = 0; e < ITS; ++e) {
-                const float4 f = ld_shared_f4(src + e * 4 * RPI * DH);
-                v[e] = make_uint4(__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z), __float_as_uint(f.w));
-            }
-            arrive_release(rempty(i));
-        };
         auto put = [&](uint32_t base, int row, const uint32_t (&x)[8]) {
             const uint32_t at_row = base + (c >> 2) * (KT * 128) + row * 128, ch = (c & 3) * 2;
 #pragma unroll
@@ -665,72 +654,73 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 else st_shared16(dst, x[0], x[1], x[2], x[3]);
             }
         };
+        // K and V by the same code (K times 1): it is half as long, and four roles share an instruction cache
         for (; run.live(); run.next()) {
             for (int k = 0; k < run.len; ++k, ++kc) {
                 look_up(kc, k == 0);
-                uint4 q[ITS];
-                // ---- K
-                uint32_t i = 2 * kc;
-                load(q, i);
-                wait_for(fempty(i), phase(i) ^ 1u, abort_flag, kErrProducer);
-                uint32_t dst = sb + P::OFF_KV + i % RING * P::KVB;
-#pragma unroll
-                for (int e = 0; e < ITS; ++e) {
-                    uint32_t x[8];
-                    to_f16x4<FMT>(q[e].x, x[0], x[1]);
-                    to_f16x4<FMT>(q[e].y, x[2], x[3]);
-                    to_f16x4<FMT>(q[e].z, x[4], x[5]);
-                    to_f16x4<FMT>(q[e].w, x[6], x[7]);
-                    put(dst, e * 4 * RPI + r0, x);
-                }
-                fence_async();
-                arrive_release(ffull(i));
-                // ---- V, scaled
-                ++i;
-                load(q, i);
-                const uint32_t dv = meta(kc) + P::M_DV + 4 * r0;
                 const float fp = ex > -1000 ? pow2i(max((FMT == FP8_E4M3 ? P::VC_E4M3 : P::VC_E5M2) - ex, -126)) : 0.0f;
-                float f[ITS];
-#pragma unroll
-                for (int e = 0; e < ITS; ++e) f[e] = __uint_as_float(ld_shared_u32(dv + e * 16 * RPI)) * fp;
+                const uint32_t dv = meta(kc) + P::M_DV + 4 * r0;
                 uint32_t all = 0xFFFFFFFFu;
 #pragma unroll
                 for (int e = 0; e < KT / 32; ++e) all &= ld_shared_u32(meta(kc) + P::M_LIVE + 4 * e);
-                if (all != 0xFFFFFFFFu || !tile_full<KT>(pv, run.u, tile_pos<KT>(run.u, run.tile + k))) {
-                    // slots that are no live position are zeros, and what only some rows see must be finite
-                    uint32_t bad = 0;
+                const bool part = all != 0xFFFFFFFFu || !tile_full<KT>(pv, run.u, tile_pos<KT>(run.u, run.tile + k));
+#pragma unroll 1
+                for (uint32_t i = 2 * kc; i < 2 * kc + 2; ++i) {
+                    const bool is_v = i & 1;
+                    wait_for(rfull(i), phase(i), abort_flag, kErrProducer);
+                    const uint32_t src = sb + P::OFF_RAW + i % RING * P::RAW + r0 * DH + 16 * c;
+                    const uint32_t dst = sb + P::OFF_KV + i % RING * P::KVB;
+                    wait_for(fempty(i), phase(i) ^ 1u, abort_flag, kErrProducer);
+#pragma unroll 1
+                    for (int e0 = 0; e0 < ITS; e0 += 4) {         // four rows' loads before their conversion
+                        uint4 q[4];
+                        float f[4] = {1.0f, 1.0f, 1.0f, 1.0f};
 #pragma unroll
-                    for (int e = 0; e < ITS; ++e) {
-                        const int r = e * 4 * RPI + r0;
-                        const bool live = (ld_shared_u32(meta(kc) + P::M_LIVE + 4 * (r >> 5)) >> (r & 31)) & 1u;
-                        if (!live) q[e] = make_uint4(0, 0, 0, 0);
-                        const uint32_t nf = nonfinite4<FMT>(q[e].x) | nonfinite4<FMT>(q[e].y) |
-                                            nonfinite4<FMT>(q[e].z) | nonfinite4<FMT>(q[e].w);
-                        if (nf || !(fabsf(f[e]) < INFINITY)) {
-                            bad = 1;
-                            auto clean = [](uint32_t x) { return x & ~((nonfinite4<FMT>(x) >> 7) * 0xFFu); };
-                            q[e] = make_uint4(clean(q[e].x), clean(q[e].y), clean(q[e].z), clean(q[e].w));
-                            if (!(fabsf(f[e]) < INFINITY)) f[e] = 0.0f;
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 w = ld_shared_f4(src + (e0 + e) * 4 * RPI * DH);
+                            q[e] = make_uint4(__float_as_uint(w.x), __float_as_uint(w.y), __float_as_uint(w.z),
+                                              __float_as_uint(w.w));
+                        }
+                        if (is_v) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                f[e] = __uint_as_float(ld_shared_u32(dv + (e0 + e) * 16 * RPI)) * fp;
+                            if (part) {
+                                // slots that are no live position are zeros, and what only some rows see must be finite
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int r = (e0 + e) * 4 * RPI + r0;
+                                    const bool live =
+                                        (ld_shared_u32(meta(kc) + P::M_LIVE + 4 * (r >> 5)) >> (r & 31)) & 1u;
+                                    if (!live) q[e] = make_uint4(0, 0, 0, 0);
+                                    const uint32_t nf = nonfinite4<FMT>(q[e].x) | nonfinite4<FMT>(q[e].y) |
+                                                        nonfinite4<FMT>(q[e].z) | nonfinite4<FMT>(q[e].w);
+                                    if (nf || !(fabsf(f[e]) < INFINITY)) {
+                                        s_poison = 1u;
+                                        auto clean = [](uint32_t x) { return x & ~((nonfinite4<FMT>(x) >> 7) * 0xFFu); };
+                                        q[e] = make_uint4(clean(q[e].x), clean(q[e].y), clean(q[e].z), clean(q[e].w));
+                                        if (!(fabsf(f[e]) < INFINITY)) f[e] = 0.0f;
+                                    }
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t x[8];
+                            to_f16x4<FMT>(q[e].x, x[0], x[1]);
+                            to_f16x4<FMT>(q[e].y, x[2], x[3]);
+                            to_f16x4<FMT>(q[e].z, x[4], x[5]);
+                            to_f16x4<FMT>(q[e].w, x[6], x[7]);
+                            const uint32_t f2 = pack_f16x2(f[e], f[e]);
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) x[y] = mul_f16x2(x[y], f2);
+                            put(dst, (e0 + e) * 4 * RPI + r0, x);
                         }
                     }
-                    if (bad) s_poison = 1u;
+                    arrive_release(rempty(i));
+                    fence_async();
+                    arrive_release(ffull(i));
                 }
-                wait_for(fempty(i), phase(i) ^ 1u, abort_flag, kErrProducer);
-                dst = sb + P::OFF_KV + i % RING * P::KVB;
-#pragma unroll
-                for (int e = 0; e < ITS; ++e) {
-                    const uint32_t f2 = pack_f16x2(f[e], f[e]);
-                    uint32_t x[8];
-                    to_f16x4<FMT>(q[e].x, x[0], x[1]);
-                    to_f16x4<FMT>(q[e].y, x[2], x[3]);
-                    to_f16x4<FMT>(q[e].z, x[4], x[5]);
-                    to_f16x4<FMT>(q[e].w, x[6], x[7]);
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) x[y] = mul_f16x2(x[y], f2);
-                    put(dst, e * 4 * RPI + r0, x);
-                }
-                fence_async();
-                arrive_release(ffull(i));
             }
         }
     } else if (wg - 1 < MT) {
@@ -740,7 +730,13 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_base + mi * P::S_COL, to = tmem + lane_base + P::O_COL + mi * DH;
         auto wg_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(2 + mi) : "memory"); };
-        const uint32_t fbuf = sb + P::OFF_F + mi * 2 * KT * 4;
+        auto wg_any = [&](bool x) {           // a barrier too
+            uint32_t r;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbar.red.or.pred q, %1, 128, p;\n\t"
+                "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"(2 + mi), "r"((uint32_t)x) : "memory");
+            return r != 0;
+        };
         uint32_t kc = 0, sc = 0;              // tiles of the CTA; S tiles of this row tile
         // the rows of this row tile in the run; Q as fp16
         int p = -1, wb = 0;
@@ -756,25 +752,40 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         };
         auto load_q = [&] {
             const Unit &u = run.u;
-            const int rho = u.rho0 + mi * 128 + row, tok = rho / a.G, g = rho - tok * a.G;
+            const int rho = u.rho0 + mi * 128 + row, tok = (int)a.gdiv.div((uint32_t)rho), g = rho - tok * a.G;
             valid = rho < u.rho1;
             p = valid ? u.n - u.count + tok : -1;
             wb = p >= 0 ? pv.window_begin(p) : 0;
             orow = (u.t0 + tok) * (int64_t)pv.H * a.G + (int64_t)run.h * a.G + g;
             // One power of two for the tile's 128 rows (an element loses something only below 2^-29 of the tile's
-            // largest, and then 2^-40 of that in the logits).
-            const __nv_bfloat16 *qp = a.q + (u.t0 + tok) * a.ld_q + (int64_t)(run.h * a.G + g) * pv.Dh;
+            // largest, and then 2^-40 of that in the logits).  A warp loads its 32 rows, whole rows at a time.
+            constexpr int QC = DH / 8, QR = 32 / QC, QN = 32 / QR;    // 16-byte chunks of a row; rows per load; loads
+            constexpr int QB = QN > 16 ? 16 : QN;                     // loads in flight
+            const int qc = lane % QC;
+            auto load_row = [&](int i) -> uint4 {
+                const int r = mi * 128 + (warp & 3) * 32 + i * QR + lane / QC, rh = u.rho0 + r;
+                if (rh >= u.rho1 || 8 * qc >= pv.Dh) return make_uint4(0, 0, 0, 0);
+                const int tk = (int)a.gdiv.div((uint32_t)rh), gg = rh - tk * a.G;
+                return *reinterpret_cast<const uint4 *>(a.q + (u.t0 + tk) * a.ld_q +
+                                                        (int64_t)(run.h * a.G + gg) * pv.Dh + 8 * qc);
+            };
+            uint4 qv[QB];
             uint32_t mx = 0;
-#pragma unroll 8
-            for (int c = 0; c < DH / 8; ++c)
-                if (valid && 8 * c < pv.Dh) mx = amax_fast8(mx, *reinterpret_cast<const uint4 *>(qp + 8 * c));
-            mx = amax_fast_final(mx);
-            if (mx == 0xFFFFFFFFu) {          // a NaN or infinity: the finite elements' maximum
-                mx = 0;
-                uint32_t bad = 0;
 #pragma unroll 1
-                for (int c = 0; c < DH / 8; ++c)
-                    if (8 * c < pv.Dh) mx = amax_exact8(mx, *reinterpret_cast<const uint4 *>(qp + 8 * c), bad);
+            for (int i0 = 0; i0 < QN; i0 += QB) {
+#pragma unroll
+                for (int i = 0; i < QB; ++i) qv[i] = load_row(i0 + i);
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < QB; ++i) m = amax_fast8(m, qv[i]);
+                m = amax_fast_final(m);
+                if (m == 0xFFFFFFFFu) {       // a NaN or infinity: the finite elements' maximum
+                    m = 0;
+                    uint32_t bad = 0;
+#pragma unroll 1
+                    for (int i = 0; i < QB; ++i) m = amax_exact8(m, load_row(i0 + i), bad);
+                }
+                mx = max(mx, m);
             }
             mx = __reduce_max_sync(0xFFFFFFFFu, mx);
             if (lane == 0) s_qmax[mi][warp & 3] = mx;
@@ -783,14 +794,17 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             const int e = max((int)(mx >> 7), 14) - 127;
             const float up = a.scale < 0.0f ? -pow2i(14 - e) : pow2i(14 - e);   // the sign of the scale goes to Q
             qf = pow2i(e) * 0x1p-14f;
-            const uint32_t qa = sb + mi * P::QB + row * 128;
-#pragma unroll 4
-            for (int c = 0; c < DH / 8; ++c) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (valid && 8 * c < pv.Dh) v = *reinterpret_cast<const uint4 *>(qp + 8 * c);
-                st_shared16(qa + (c >> 3) * (128 * 128) + (((c & 7) ^ (row & 7)) << 4),
-                            pack_f16x2(bf_lo(v.x) * up, bf_hi(v.x) * up), pack_f16x2(bf_lo(v.y) * up, bf_hi(v.y) * up),
-                            pack_f16x2(bf_lo(v.z) * up, bf_hi(v.z) * up), pack_f16x2(bf_lo(v.w) * up, bf_hi(v.w) * up));
+#pragma unroll 1
+            for (int i0 = 0; i0 < QN; i0 += QB) {
+#pragma unroll
+                for (int i = 0; i < QB; ++i) {
+                    if (QN > QB) qv[i] = load_row(i0 + i);
+                    const uint4 v = qv[i];
+                    const int r = (warp & 3) * 32 + (i0 + i) * QR + lane / QC;
+                    st_shared16(sb + mi * P::QB + (qc >> 3) * (128 * 128) + r * 128 + (((qc & 7) ^ (r & 7)) << 4),
+                                pack_f16x2(bf_lo(v.x) * up, bf_hi(v.x) * up), pack_f16x2(bf_lo(v.y) * up, bf_hi(v.y) * up),
+                                pack_f16x2(bf_lo(v.z) * up, bf_hi(v.z) * up), pack_f16x2(bf_lo(v.w) * up, bf_hi(v.w) * up));
+                }
             }
             fence_async();
             arrive_release(qfull(mi));
@@ -803,61 +817,73 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             float mr = kNoMax, l = 0.0f;
             int ex = -1000;
             for (int k = 0; k < len; ++k, ++kc, ++sc) {
-                const uint32_t m = sb + P::OFF_M + (kc % P::META) * P::M_BYTES, fk = fbuf + (kc & 1) * KT * 4;
+                const uint32_t m = sb + P::OFF_M + (kc % P::META) * P::M_BYTES;
+                const float4 *fk = s_factor[mi][kc & 1];
                 const int j0 = tile_pos<KT>(u, tile + k);
                 // The columns' factors, before S is ready where their look-up can be waited for: from the second
                 // tile of a run on, when the one before it in the ring is known to be past (a parity only tells a
                 // phase from its neighbours); S of the first tile is behind its look-up.
                 if (k == 0) wait_for(sfull(mi), sc & 1u, abort_flag, kErrEpilogue);
                 else wait_for(mfull(kc), (kc / P::META) & 1u, abort_flag, kErrEpilogue);
-                if (row < KT)
-                    st_shared_u32(fk + 4 * row, __float_as_uint(__uint_as_float(ld_shared_u32(m + P::M_DK + 4 * row)) * qf));
-                wg_sync();
-                uint32_t live[KT / 32], all = 0xFFFFFFFFu;
+                const float fcol = row < KT ? __uint_as_float(ld_shared_u32(m + P::M_DK + 4 * row)) * qf : 1.0f;
+                // a factor that is no positive number is dealt with column by column below
+                const bool odd = !(fcol > 0.0f && fcol < INFINITY);
+                if (row < KT) reinterpret_cast<float *>(s_factor[mi][kc & 1])[row] = odd ? 1.0f : fcol;
+                uint32_t all = 0xFFFFFFFFu;
 #pragma unroll
-                for (int i = 0; i < KT / 32; ++i) all &= live[i] = ld_shared_u32(m + P::M_LIVE + 4 * i);
-                const bool masked = all != 0xFFFFFFFFu || !tile_full<KT>(pv, u, j0);
+                for (int i = 0; i < KT / 32; ++i) all &= ld_shared_u32(m + P::M_LIVE + 4 * i);
+                const bool odd_column =
+                    wg_any(odd && ((ld_shared_u32(m + P::M_LIVE + 4 * ((row % KT) >> 5)) >> (row & 31)) & 1u));
+                const bool masked = odd_column || all != 0xFFFFFFFFu || !tile_full<KT>(pv, u, j0);
                 if (k > 0) wait_for(sfull(mi), sc & 1u, abort_flag, kErrEpilogue);
                 tc_fence_after();
-                // what the row does not see of 32 columns
-                auto hide = [&](uint32_t (&x)[32], int i) {
-                    const int c0 = j0 + 32 * i;
-                    const uint32_t see = below(p + 1 - c0) & (~below(wb - c0) | below(pv.sinks - c0)) & live[i];
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (!((see >> c) & 1u)) x[c] = 0xFF800000u;   // -inf
-                };
                 // The first tile's maximum sets the reference before any weight is taken.  Later tiles take their
                 // weights against the reference they find, and their sum tells afterwards whether one may have passed
                 // 2^15: P waits in registers (S's columns become P's), and such a tile is done again.
                 uint32_t pk[KT / 2];
                 float al = 1.0f, sum = 0.0f;
-                bool first = k == 0, bad = first;
+                bool again = k == 0, bad = again, hide = masked;
                 while (true) {
-                    if (__any_sync(0xFFFFFFFFu, bad)) {
+                    if (hide || __any_sync(0xFFFFFFFFu, bad)) {
+                        // The maximum; and into S, -inf for what the row does not see and the product where the
+                        // column's factor is odd, so that the sweep needs no mask.
                         float top = -INFINITY;
 #pragma unroll 1
                         for (int i = 0; i < KT / 32; ++i) {
+                            const int c0 = j0 + 32 * i;
+                            const uint32_t see = below(p + 1 - c0) & (~below(wb - c0) | below(pv.sinks - c0)) &
+                                                 ld_shared_u32(m + P::M_LIVE + 4 * i);
                             uint32_t x[32];
                             tmem_ld32_async(ts + 32 * i, x);
                             tmem_ld_wait(x);
+                            if (hide) {
+                                if (odd_column) {
+#pragma unroll
+                                    for (int c = 0; c < 32; ++c) {
+                                        const float o = __uint_as_float(ld_shared_u32(m + P::M_DK + 4 * (32 * i + c))) * qf;
+                                        if (!(o > 0.0f && o < INFINITY)) x[c] = __float_as_uint(__uint_as_float(x[c]) * o);
+                                    }
+                                }
+#pragma unroll
+                                for (int c = 0; c < 32; ++c)
+                                    if (!((see >> c) & 1u)) x[c] = 0xFF800000u;   // -inf
+                                tmem_st16(ts + 32 * i, x);
+                                tmem_st16(ts + 32 * i + 16, x + 16);
+                            }
 #pragma unroll
                             for (int c = 0; c < 32; c += 4) {
-                                const float4 f = ld_shared_f4(fk + 4 * (32 * i + c));
-                                x[c] = __float_as_uint(__uint_as_float(x[c]) * f.x);
-                                x[c + 1] = __float_as_uint(__uint_as_float(x[c + 1]) * f.y);
-                                x[c + 2] = __float_as_uint(__uint_as_float(x[c + 2]) * f.z);
-                                x[c + 3] = __float_as_uint(__uint_as_float(x[c + 3]) * f.w);
+                                const float4 f = fk[8 * i + c / 4];
+                                top = fmaxf(top, fmaxf(__uint_as_float(x[c]) * f.x, __uint_as_float(x[c + 1]) * f.y));
+                                top = fmaxf(top, fmaxf(__uint_as_float(x[c + 2]) * f.z, __uint_as_float(x[c + 3]) * f.w));
                             }
-                            if (masked) hide(x, i);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) top = fmaxf(top, __uint_as_float(x[c]));
                         }
+                        if (hide) tmem_st_wait();
                         if (bad && top > kNoMax) {
                             al = exp2_fast(mr - (top - kBelow));
                             mr = top - kBelow;
                         }
-                        first = true;
+                        if (__any_sync(0xFFFFFFFFu, bad)) again = true;
+                        hide = false;
                     }
                     const uint64_t mr2 = pack_ff(-mr, -mr);
                     uint64_t acc[2] = {0ull, 0ull};
@@ -871,28 +897,25 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                         if (i + 1 < KT / 32) tmem_ld32_async(ts + 32 * (i + 1), nx);
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
-                            const float4 f = ld_shared_f4(fk + 4 * (32 * i + c));
-                            const uint64_t lo = fma_f32x2(pack_f32x2(x[c], x[c + 1]), pack_ff(f.x, f.y), mr2);
-                            const uint64_t hi = fma_f32x2(pack_f32x2(x[c + 2], x[c + 3]), pack_ff(f.z, f.w), mr2);
-                            x[c] = (uint32_t)lo;
-                            x[c + 1] = (uint32_t)(lo >> 32);
-                            x[c + 2] = (uint32_t)hi;
-                            x[c + 3] = (uint32_t)(hi >> 32);
-                        }
-                        if (masked) hide(x, i);
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            const float e0 = exp2_fast(__uint_as_float(x[2 * c]));
-                            const float e1 = exp2_fast(__uint_as_float(x[2 * c + 1]));
-                            acc[c & 1] = add_f32x2(acc[c & 1], pack_ff(e0, e1));
-                            pk[16 * i + c] = pack_f16x2(e0, e1);
+                            const float4 f = fk[(32 * i + c) / 4];
+                            float e0, e1, e2, e3;
+                            unpack_f32x2(fma_f32x2(pack_f32x2(x[c], x[c + 1]), pack_ff(f.x, f.y), mr2), e0, e1);
+                            unpack_f32x2(fma_f32x2(pack_f32x2(x[c + 2], x[c + 3]), pack_ff(f.z, f.w), mr2), e2, e3);
+                            e0 = exp2_fast(e0);
+                            e1 = exp2_fast(e1);
+                            e2 = exp2_fast(e2);
+                            e3 = exp2_fast(e3);
+                            acc[0] = add_f32x2(acc[0], pack_ff(e0, e1));
+                            acc[1] = add_f32x2(acc[1], pack_ff(e2, e3));
+                            pk[(32 * i + c) / 2] = pack_f16x2(e0, e1);
+                            pk[(32 * i + c) / 2 + 1] = pack_f16x2(e2, e3);
                         }
                     }
                     float s0, s1;
                     unpack_f32x2(add_f32x2(acc[0], acc[1]), s0, s1);
                     sum = s0 + s1;
                     bad = !(sum < kMaxSum);
-                    if (first || !__any_sync(0xFFFFFFFFu, bad)) break;   // a second NaN or infinity is the result
+                    if (again || !__any_sync(0xFFFFFFFFu, bad)) break;   // a second NaN or infinity is the result
                 }
                 l = l * al + sum;
                 // ---- O against the new reference and V's exponent
@@ -1178,6 +1201,7 @@ extern "C" fp8_status fp8_paged_attention_prefill(
     a.T = T;
     a.B = (int)B;
     a.G = (int)(Hq / H);
+    a.gdiv = make_fastdiv((uint32_t)a.G);
     a.ctas = p.ctas;
     a.max_blocks = p.blocks;
     a.box = block_size % 32 == 0 ? 32 : block_size % 16 == 0 ? 16 : 8;
