@@ -757,35 +757,41 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             p = valid ? u.n - u.count + tok : -1;
             wb = p >= 0 ? pv.window_begin(p) : 0;
             orow = (u.t0 + tok) * (int64_t)pv.H * a.G + (int64_t)run.h * a.G + g;
-            // One power of two for the tile's 128 rows (an element loses something only below 2^-29 of the tile's
-            // largest, and then 2^-40 of that in the logits).  A warp loads its 32 rows, whole rows at a time.
-            constexpr int QC = DH / 8, QR = 32 / QC, QN = 32 / QR;    // 16-byte chunks of a row; rows per load; loads
-            constexpr int QB = QN > 16 ? 16 : QN;                     // loads in flight
-            const int qc = lane % QC;
-            auto load_row = [&](int i) -> uint4 {
-                const int r = mi * 128 + (warp & 3) * 32 + i * QR + lane / QC, rh = u.rho0 + r;
-                if (rh >= u.rho1 || 8 * qc >= pv.Dh) return make_uint4(0, 0, 0, 0);
-                const int tk = (int)a.gdiv.div((uint32_t)rh), gg = rh - tk * a.G;
-                return *reinterpret_cast<const uint4 *>(a.q + (u.t0 + tk) * a.ld_q +
-                                                        (int64_t)(run.h * a.G + gg) * pv.Dh + 8 * qc);
+            // A warp copies its 32 rows as they are, whole rows at a time, then scales them in place, each thread what
+            // it copied; short loops, since code that runs once per unit comes from far away.  One power of two for
+            // the tile's 128 rows (an element loses something only below 2^-29 of the tile's largest, and then 2^-40
+            // of that in the logits).
+            constexpr int QC = DH / 8, QR = 32 / QC, QN = 32 / QR;    // 16-byte chunks of a row; rows per copy; copies
+            const int qc = lane % QC, r0 = (warp & 3) * 32 + lane / QC;
+            auto at_row = [&](int i) -> uint32_t {
+                const int r = r0 + i * QR;
+                return sb + mi * P::QB + (qc >> 3) * (128 * 128) + r * 128 + (((qc & 7) ^ (r & 7)) << 4);
             };
-            uint4 qv[QB];
+            const __nv_bfloat16 *qp = a.q + u.t0 * a.ld_q + (int64_t)run.h * a.G * pv.Dh + 8 * qc;
+#pragma unroll 2
+            for (int i = 0; i < QN; ++i) {
+                const int rh = u.rho0 + mi * 128 + r0 + i * QR;
+                const bool there = rh < u.rho1 && 8 * qc < pv.Dh;
+                const int tk = (int)a.gdiv.div((uint32_t)rh), gg = rh - tk * a.G;
+                const __nv_bfloat16 *src = there ? qp + tk * a.ld_q + gg * pv.Dh : a.q;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at_row(i)), "l"(src),
+                             "r"(there ? 16 : 0)
+                             : "memory");
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            auto own = [&](int i) -> uint4 {
+                const float4 w = ld_shared_f4(at_row(i));
+                return make_uint4(__float_as_uint(w.x), __float_as_uint(w.y), __float_as_uint(w.z), __float_as_uint(w.w));
+            };
             uint32_t mx = 0;
+#pragma unroll 4
+            for (int i = 0; i < QN; ++i) mx = amax_fast8(mx, own(i));
+            mx = amax_fast_final(mx);
+            if (mx == 0xFFFFFFFFu) {          // a NaN or infinity: the finite elements' maximum
+                mx = 0;
+                uint32_t bad = 0;
 #pragma unroll 1
-            for (int i0 = 0; i0 < QN; i0 += QB) {
-#pragma unroll
-                for (int i = 0; i < QB; ++i) qv[i] = load_row(i0 + i);
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < QB; ++i) m = amax_fast8(m, qv[i]);
-                m = amax_fast_final(m);
-                if (m == 0xFFFFFFFFu) {       // a NaN or infinity: the finite elements' maximum
-                    m = 0;
-                    uint32_t bad = 0;
-#pragma unroll 1
-                    for (int i = 0; i < QB; ++i) m = amax_exact8(m, load_row(i0 + i), bad);
-                }
-                mx = max(mx, m);
+                for (int i = 0; i < QN; ++i) mx = amax_exact8(mx, own(i), bad);
             }
             mx = __reduce_max_sync(0xFFFFFFFFu, mx);
             if (lane == 0) s_qmax[mi][warp & 3] = mx;
@@ -794,17 +800,12 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             const int e = max((int)(mx >> 7), 14) - 127;
             const float up = a.scale < 0.0f ? -pow2i(14 - e) : pow2i(14 - e);   // the sign of the scale goes to Q
             qf = pow2i(e) * 0x1p-14f;
-#pragma unroll 1
-            for (int i0 = 0; i0 < QN; i0 += QB) {
-#pragma unroll
-                for (int i = 0; i < QB; ++i) {
-                    if (QN > QB) qv[i] = load_row(i0 + i);
-                    const uint4 v = qv[i];
-                    const int r = (warp & 3) * 32 + (i0 + i) * QR + lane / QC;
-                    st_shared16(sb + mi * P::QB + (qc >> 3) * (128 * 128) + r * 128 + (((qc & 7) ^ (r & 7)) << 4),
-                                pack_f16x2(bf_lo(v.x) * up, bf_hi(v.x) * up), pack_f16x2(bf_lo(v.y) * up, bf_hi(v.y) * up),
-                                pack_f16x2(bf_lo(v.z) * up, bf_hi(v.z) * up), pack_f16x2(bf_lo(v.w) * up, bf_hi(v.w) * up));
-                }
+#pragma unroll 2
+            for (int i = 0; i < QN; ++i) {
+                const uint4 v = own(i);
+                st_shared16(at_row(i), pack_f16x2(bf_lo(v.x) * up, bf_hi(v.x) * up),
+                            pack_f16x2(bf_lo(v.y) * up, bf_hi(v.y) * up), pack_f16x2(bf_lo(v.z) * up, bf_hi(v.z) * up),
+                            pack_f16x2(bf_lo(v.w) * up, bf_hi(v.w) * up));
             }
             fence_async();
             arrive_release(qfull(mi));
@@ -962,7 +963,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             tc_fence_after();
             constexpr int vc = FMT == FP8_E4M3 ? P::VC_E4M3 : P::VC_E5M2;
             const float fo = ex > -1000 ? pow2i(min(ex - vc, 127)) : 0.0f;
-            const float r = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+            const float r = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f, by = fo * r;   // a weighted mean's scale: no overflow
             float *part = a.part + ((int64_t)blockIdx.x * 2 + (tile == 0 ? 1 : 0)) * ((int64_t)ROWS * (DH + 2));
             const bool poison = *reinterpret_cast<volatile uint32_t *>(&s_poison) != 0u;
 #pragma unroll 1
@@ -972,7 +973,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 tmem_ld_wait(o);
                 float v[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * fo;
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * by;
                 if (poison) {
                     // values that were taken out of V: back into the rows that see them
 #pragma unroll 1
@@ -1002,10 +1003,10 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                     for (int i = 0; i < 32; i += 8)
                         if (c + i < pv.Dh) {
                             uint4 w;
-                            w.x = pack_bf16x2(v[i] * r, v[i + 1] * r);
-                            w.y = pack_bf16x2(v[i + 2] * r, v[i + 3] * r);
-                            w.z = pack_bf16x2(v[i + 4] * r, v[i + 5] * r);
-                            w.w = pack_bf16x2(v[i + 6] * r, v[i + 7] * r);
+                            w.x = pack_bf16x2(v[i], v[i + 1]);
+                            w.y = pack_bf16x2(v[i + 2], v[i + 3]);
+                            w.z = pack_bf16x2(v[i + 4], v[i + 5]);
+                            w.w = pack_bf16x2(v[i + 6], v[i + 7]);
                             *reinterpret_cast<uint4 *>(op + i) = w;
                         }
                 } else {
