@@ -630,8 +630,8 @@ FP8Q_API fp8_status fp8_paged_attention_workspace_size(int64_t B, int64_t Hq, in
  *   mass_out    [B, H, ld_out] fp32, not overlapping mass: the kept tokens'
  *               masses (those of positions below ld_out), then zeros.
  *   lens_out    [B] int32: min(n, budget); may be seq_lens itself.
- *   Shapes: Dh % 8 == 0, H * Dh <= 8192, B <= 65535, budget >= 1, sinks and
- *   recent >= 0, sinks + recent <= budget, num_blocks * block_size < 2^31,
+ *   Shapes: Dh % 8 == 0, H * Dh <= 8192, B <= 65535, 1 <= budget <= 2^31 -
+ *   65536, sinks and recent >= 0, sinks + recent <= budget, num_blocks * block_size < 2^31,
  *   max_blocks * block_size and dst_max_blocks * block_size <= 2^31 - 65536.
  *   Errors: FP8_ERR_SHAPE, FP8_ERR_INVALID_ARG (NULL pointer),
  *   FP8_ERR_ALIGNMENT (the caches: 16 bytes).
