@@ -277,9 +277,31 @@ struct Runs {
 };
 
 // --------------------------------------------------------------- PTX glue --
+// Bounded wait, as wait_bar(), for warps that share their scheduler with others that work: a try sleeps up to
+// 20 us unless the phase completes, and nobody waits again after a wait that ran out.
+__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag, uint32_t code) {
-    if (*abort_flag) return false;    // after a wait that ran out nobody waits again
-    return wait_bar(bar, parity, abort_flag, code);
+    if (try_wait_long(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    while (!try_wait_long(bar, parity)) {
+        if (*abort_flag) return false;
+        if (globaltimer() - t0 > kTimeoutNs) {
+            atomicOr(&g_gemm_error, code);
+            *abort_flag = 1u;
+            return false;
+        }
+    }
+    return true;
 }
 __device__ __forceinline__ void arrive_release(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -329,6 +351,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+__device__ __forceinline__ void tmem_ld16_async(uint32_t addr, uint32_t *o) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]),
+          "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+        : "r"(addr));
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // waits for the loads in flight; the registers of this array cannot be read above it
@@ -888,17 +918,17 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                     }
                     const uint64_t mr2 = pack_ff(-mr, -mr);
                     uint64_t acc[2] = {0ull, 0ull};
-                    uint32_t xa[32], xb[32];
-                    tmem_ld32_async(ts, xa);
+                    uint32_t xa[16], xb[16];
+                    tmem_ld16_async(ts, xa);
 #pragma unroll
-                    for (int i = 0; i < KT / 32; ++i) {
+                    for (int i = 0; i < KT / 16; ++i) {
                         auto &x = i & 1 ? xb : xa;
                         auto &nx = i & 1 ? xa : xb;
                         tmem_ld_wait(x);
-                        if (i + 1 < KT / 32) tmem_ld32_async(ts + 32 * (i + 1), nx);
+                        if (i + 1 < KT / 16) tmem_ld16_async(ts + 16 * (i + 1), nx);
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            const float4 f = fk[(32 * i + c) / 4];
+                        for (int c = 0; c < 16; c += 4) {
+                            const float4 f = fk[(16 * i + c) / 4];
                             float e0, e1, e2, e3;
                             unpack_f32x2(fma_f32x2(pack_f32x2(x[c], x[c + 1]), pack_ff(f.x, f.y), mr2), e0, e1);
                             unpack_f32x2(fma_f32x2(pack_f32x2(x[c + 2], x[c + 3]), pack_ff(f.z, f.w), mr2), e2, e3);
@@ -908,8 +938,8 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                             e3 = exp2_fast(e3);
                             acc[0] = add_f32x2(acc[0], pack_ff(e0, e1));
                             acc[1] = add_f32x2(acc[1], pack_ff(e2, e3));
-                            pk[(32 * i + c) / 2] = pack_f16x2(e0, e1);
-                            pk[(32 * i + c) / 2 + 1] = pack_f16x2(e2, e3);
+                            pk[(16 * i + c) / 2] = pack_f16x2(e0, e1);
+                            pk[(16 * i + c) / 2 + 1] = pack_f16x2(e2, e3);
                         }
                     }
                     float s0, s1;
@@ -928,13 +958,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
 #pragma unroll 1
                     for (int c = 0; c < DH; c += 16) {
                         uint32_t o[16];
-                        asm volatile(
-                            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                            : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
-                              "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
-                              "=r"(o[14]), "=r"(o[15])
-                            : "r"(to + c));
+                        tmem_ld16_async(to + c, o);
                         tmem_ld_wait(o);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
