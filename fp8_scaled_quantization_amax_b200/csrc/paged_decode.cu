@@ -325,6 +325,7 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
                 const uint32_t mask = __ballot_sync(0xFFFFFFFFu, live);
                 const uint32_t dst = data + (uint32_t)(fill * C::UNIT), ax = aux + (uint32_t)(fill * C::AUX);
                 if constexpr (TMA) {
+                  if (!*reinterpret_cast<volatile uint32_t *>(&s_abort)) {   // after a wait that ran out: no more copies
                     const uint32_t bar = bars + 8 * fill;
                     if (lane == 0) mbar_expect_tx(bar, C::UNIT);
                     if ((lane & (a.box - 1)) == 0) {
@@ -334,6 +335,7 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
                         tma_load_3d(dst + (uint32_t)(lane * (DH == 64 ? 64 : 128)), map, bar, 0, h, z);
                         if (DH == 256) tma_load_3d(dst + 4096u + (uint32_t)(lane * 128), map, bar, 128, h, z);
                     }
+                  }
                 } else {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {

@@ -303,6 +303,22 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
     }
     return true;
 }
+// Bounded wait until the count at addr has reached n (n <= 0: at once).
+__device__ __forceinline__ void wait_progress(uint32_t addr, uint32_t n, volatile uint32_t *abort_flag) {
+    uint64_t t0 = 0;
+    while (true) {
+        uint32_t v;
+        asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+        if ((int)(v - n) >= 0 || *abort_flag) return;
+        if (t0 == 0) t0 = globaltimer();
+        else if (globaltimer() - t0 > kTimeoutNs) {
+            atomicOr(&g_gemm_error, kErrProducer);
+            *abort_flag = 1u;
+            return;
+        }
+        __nanosleep(200);
+    }
+}
 __device__ __forceinline__ void arrive_release(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -341,6 +357,15 @@ __device__ __forceinline__ void commit_one(uint32_t bar, uint32_t leader) {
         "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
         "r"(leader)
+        : "memory");
+}
+// A predicate here too: in a branch of its own the leader would fall behind lanes that already wait for what it is
+// to commit.
+__device__ __forceinline__ void st_release_one(uint32_t addr, uint32_t v, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q st.release.cta.shared::cta.u32 [%0], %1;\n\t}" ::"r"(addr),
+        "r"(v), "r"(leader)
         : "memory");
 }
 // 32 lanes x 16 columns from registers; tmem_st_wait() before they are read
@@ -462,6 +487,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // s_poison: something was taken out of V (for good: later results of this CTA look again for nothing)
     __shared__ uint32_t s_tmem, s_abort, s_poison, s_qmax[MT][4];
+    __shared__ uint32_t s_progress;   // tiles whose weights all softmax warps have handed over
     __shared__ float4 s_factor[MT][2][KT / 4];   // column factors of a row tile's softmax, two tiles
     volatile uint32_t *abort_flag = &s_abort;
     const uint32_t sb = smem_u32(smem);
@@ -495,7 +521,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         }
         for (int i = 0; i < P::META; ++i) mbar_init(mfull(i), 32);
         mbar_init(drain, 1);
-        s_abort = s_poison = 0u;
+        s_abort = s_poison = s_progress = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -560,7 +586,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                     if (!ok) break;
                     if (k >= 0) {
                         commit_one(fempty(vi), leader);
-                        ++kc;
+                        st_release_one(smem_u32(&s_progress), ++kc, leader);
                     }
                     if (k + 1 < len) commit_one(fempty(ki), leader);
                 }
@@ -570,13 +596,17 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             __syncwarp();
         } else if (warp == 1) {
             // -------------------------- codes of the tiles, K and V in turn --
-            uint32_t kc = 0;
-            for (; run.live(); run.next()) {
-                for (int k = 0; k < run.len; ++k, ++kc) {
-                    wait_for(mfull(kc), (kc / P::META) & 1u, abort_flag, kErrProducer);
+            uint32_t kc = 0, issued = 0;
+            bool ok = true;                   // after a wait that ran out nothing more is copied
+            for (; ok && run.live(); run.next()) {
+                for (int k = 0; ok && k < run.len; ++k, ++kc) {
+                    ok = wait_for(mfull(kc), (kc / P::META) & 1u, abort_flag, kErrProducer);
                     const uint32_t slots = sb + P::OFF_M + (kc % P::META) * P::M_BYTES + P::M_SLOT;
-                    for (uint32_t i = 2 * kc; i < 2 * kc + 2; ++i) {
-                        wait_for(rempty(i), phase(i) ^ 1u, abort_flag, kErrProducer);
+                    for (uint32_t i = 2 * kc; ok && i < 2 * kc + 2; ++i) {
+                        ok = wait_for(rempty(i), phase(i) ^ 1u, abort_flag, kErrProducer) && !*abort_flag;
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        issued = i + 1;
                         const uint32_t dst = sb + P::OFF_RAW + i % RING * P::RAW;
                         if constexpr (TMA) {
                             if (lane == 0) mbar_expect_tx(rfull(i), P::RAW);
@@ -605,6 +635,9 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 }
             }
             if constexpr (!TMA) asm volatile("cp.async.wait_all;" ::: "memory");
+            // copies that the converter may not have waited for end before the CTA does
+            if (TMA && *abort_flag)
+                for (uint32_t i = issued > RING ? issued - RING : 0; i < issued; ++i) wait_bar_drain(rfull(i), phase(i));
             __syncwarp();
         } else {
             // ------------------------- slots, scales and masks of tiles ---
@@ -615,14 +648,10 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 const Unit &u = run.u;
                 const int h = run.h;
                 for (int k = 0; k < run.len; ++k, ++kc) {
-                    // S of tile kc - 5 is issued behind the softmax of tile kc - 6: nobody reads kc - 8 any more.
-                    // Both warps wait for every buffer: a parity only tells a phase from its neighbours.
-                    if (kc >= 5) {
-                        const uint32_t i = 2 * (kc - 5);
-                        if (i > 0) wait_for(fempty(i - 1), phase(i - 1), abort_flag, kErrProducer);
-                        wait_for(fempty(i), phase(i), abort_flag, kErrProducer);
-                    }
                     if ((kc & 1) != (uint32_t)(warp & 1)) continue;
+                    // Nobody reads tile kc - META any more: a count, because a parity only tells a phase from its
+                    // neighbours and this warp may come much later than the phase it would wait for.
+                    wait_progress(smem_u32(&s_progress), kc + 1 - P::META, abort_flag);
                     uint8_t *m = smem + P::OFF_M + (kc % P::META) * P::M_BYTES;
                     const int j0 = tile_pos<KT>(u, run.tile + k);
                     int s[KT / 32];

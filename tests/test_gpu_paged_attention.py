@@ -159,6 +159,24 @@ def test_prefill_rows_of_no_sequence_are_left_alone_and_short_sequences_see_noth
     check_rows(out, lse, q, k, v, table, lens, rows, 0.125, 0, 0, scaled_v=True)
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 5)])
+def test_prefill_with_many_tiles_and_units_per_cta(window, sinks):
+    """Long sequences on many heads (every CTA goes through many units and tiles), checked on sampled rows, twice."""
+    seqs = [(5000, 1025), (3001, 64), (700, 700), (4100, 513)]
+    lens = [n for n, _ in seqs]
+    H, G, Dh = 8, 4, 128
+    k, v, table, ln = make_caches(lens, H, Dh, 32, 0, seed=77)
+    off = torch.tensor([0] + [m for _, m in seqs]).cumsum(0)
+    q = inputs.normal_bf16((int(off[-1]), H * G, Dh), 1.0, seed=6).to(DEV)
+    out, lse = fp8q.paged_attention_prefill(q, off.to(DEV), k, v, table, ln, window, sinks)
+    again, lse2 = fp8q.paged_attention_prefill(q, off.to(DEV), k, v, table, ln, window, sinks)
+    torch.cuda.synchronize()
+    assert fp8q.fp8_device_error() == 0
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    rows = [(int(off[b]) + i, b, n - m + i) for b, (n, m) in enumerate(seqs) for i in (0, 1, m // 3, m - 2, m - 1)]
+    check_rows(out, lse, q, k, v, table, lens, rows, Dh ** -0.5, window, sinks, scaled_v=True)
+
+
 def test_prefill_of_one_token_agrees_with_decode():
     lens = [300, 17]
     k, v, table, ln = make_caches(lens, 2, 128, 16, 0, seed=11)
