@@ -705,13 +705,8 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         };
         auto put = [&](uint32_t base, int row, const uint32_t (&x)[8]) {
             const uint32_t at_row = base + (c >> 2) * (KT * 128) + row * 128, ch = (c & 3) * 2;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int hf = e ^ swap;
-                const uint32_t dst = at_row + (((ch + hf) ^ (row & 7)) << 4);
-                if (hf) st_shared16(dst, x[4], x[5], x[6], x[7]);
-                else st_shared16(dst, x[0], x[1], x[2], x[3]);
-            }
+            st_shared16(at_row + (((ch + swap) ^ (row & 7)) << 4), x[0], x[1], x[2], x[3]);
+            st_shared16(at_row + (((ch + 1 - swap) ^ (row & 7)) << 4), x[4], x[5], x[6], x[7]);
         };
         // K and V by the same code (K times 1): it is half as long, and four roles share an instruction cache
         for (; run.live(); run.next()) {
@@ -737,8 +732,8 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float4 w = ld_shared_f4(src + (e0 + e) * 4 * RPI * DH);
-                            q[e] = make_uint4(__float_as_uint(w.x), __float_as_uint(w.y), __float_as_uint(w.z),
-                                              __float_as_uint(w.w));
+                            q[e] = make_uint4(__float_as_uint(swap ? w.z : w.x), __float_as_uint(swap ? w.w : w.y),
+                                              __float_as_uint(swap ? w.x : w.z), __float_as_uint(swap ? w.y : w.w));
                         }
                         if (is_v) {
 #pragma unroll
@@ -878,7 +873,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             int ex = -1000;
             for (int k = 0; k < len; ++k, ++kc, ++sc) {
                 const uint32_t m = sb + P::OFF_M + (kc % P::META) * P::M_BYTES;
-                const float4 *fk = s_factor[mi][kc & 1];
+                const uint32_t fk = smem_u32(s_factor[mi][kc & 1]);
                 const int j0 = tile_pos<KT>(u, tile + k);
                 // The columns' factors, before S is ready where their look-up can be waited for: from the second
                 // tile of a run on, when the one before it in the ring is known to be past (a parity only tells a
@@ -897,6 +892,10 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 const bool masked = odd_column || all != 0xFFFFFFFFu || !tile_full<KT>(pv, u, j0);
                 if (k > 0) wait_for(sfull(mi), sc & 1u, abort_flag, kErrEpilogue);
                 tc_fence_after();
+                if (!__any_sync(0xFFFFFFFFu, valid)) {       // P is whatever S holds: it only reaches O's rows of no one
+                    arrive_release(pfull(mi));
+                    continue;
+                }
                 // The first tile's maximum sets the reference before any weight is taken.  Later tiles take their
                 // weights against the reference they find, and their sum tells afterwards whether one may have passed
                 // 2^15: P waits in registers (S's columns become P's), and such a tile is done again.
@@ -904,7 +903,8 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 float al = 1.0f, sum = 0.0f;
                 bool again = k == 0, bad = again, hide = masked;
                 while (true) {
-                    if (hide || __any_sync(0xFFFFFFFFu, bad)) {
+                    const bool raise = __any_sync(0xFFFFFFFFu, bad);
+                    if (hide || raise) {
                         // The maximum; and into S, -inf for what the row does not see and the product where the
                         // column's factor is odd, so that the sweep needs no mask.
                         float top = -INFINITY;
@@ -930,9 +930,10 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                                 tmem_st16(ts + 32 * i, x);
                                 tmem_st16(ts + 32 * i + 16, x + 16);
                             }
+                            if (!raise) continue;
 #pragma unroll
                             for (int c = 0; c < 32; c += 4) {
-                                const float4 f = fk[8 * i + c / 4];
+                                const float4 f = ld_shared_f4(fk + 128 * i + 4 * c);
                                 top = fmaxf(top, fmaxf(__uint_as_float(x[c]) * f.x, __uint_as_float(x[c + 1]) * f.y));
                                 top = fmaxf(top, fmaxf(__uint_as_float(x[c + 2]) * f.z, __uint_as_float(x[c + 3]) * f.w));
                             }
@@ -942,33 +943,39 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                             al = exp2_fast(mr - (top - kBelow));
                             mr = top - kBelow;
                         }
-                        if (__any_sync(0xFFFFFFFFu, bad)) again = true;
+                        again |= raise;
                         hide = false;
                     }
                     const uint64_t mr2 = pack_ff(-mr, -mr);
                     uint64_t acc[2] = {0ull, 0ull};
                     uint32_t xa[16], xb[16];
+                    float ya[16], yb[16];
                     tmem_ld16_async(ts, xa);
 #pragma unroll
-                    for (int i = 0; i < KT / 16; ++i) {
+                    for (int i = 0; i <= KT / 16; ++i) {
                         auto &x = i & 1 ? xb : xa;
                         auto &nx = i & 1 ? xa : xb;
-                        tmem_ld_wait(x);
-                        if (i + 1 < KT / 16) tmem_ld16_async(ts + 16 * (i + 1), nx);
+                        auto &y = i & 1 ? yb : ya;
+                        auto &py = i & 1 ? ya : yb;
+                        if (i < KT / 16) {
+                            tmem_ld_wait(x);
+                            if (i + 1 < KT / 16) tmem_ld16_async(ts + 16 * (i + 1), nx);
+                        }
 #pragma unroll
                         for (int c = 0; c < 16; c += 4) {
-                            const float4 f = fk[(16 * i + c) / 4];
-                            float e0, e1, e2, e3;
-                            unpack_f32x2(fma_f32x2(pack_f32x2(x[c], x[c + 1]), pack_ff(f.x, f.y), mr2), e0, e1);
-                            unpack_f32x2(fma_f32x2(pack_f32x2(x[c + 2], x[c + 3]), pack_ff(f.z, f.w), mr2), e2, e3);
-                            e0 = exp2_fast(e0);
-                            e1 = exp2_fast(e1);
-                            e2 = exp2_fast(e2);
-                            e3 = exp2_fast(e3);
-                            acc[0] = add_f32x2(acc[0], pack_ff(e0, e1));
-                            acc[1] = add_f32x2(acc[1], pack_ff(e2, e3));
-                            pk[(16 * i + c) / 2] = pack_f16x2(e0, e1);
-                            pk[(16 * i + c) / 2 + 1] = pack_f16x2(e2, e3);
+                            if (i < KT / 16) {
+                                const float4 f = ld_shared_f4(fk + 64 * i + 4 * c);
+                                unpack_f32x2(fma_f32x2(pack_f32x2(x[c], x[c + 1]), pack_ff(f.x, f.y), mr2), y[c], y[c + 1]);
+                                unpack_f32x2(fma_f32x2(pack_f32x2(x[c + 2], x[c + 3]), pack_ff(f.z, f.w), mr2), y[c + 2], y[c + 3]);
+#pragma unroll
+                                for (int e = c; e < c + 4; ++e) y[e] = exp2_fast(y[e]);
+                            }
+                            if (i > 0) {
+                                acc[0] = add_f32x2(acc[0], pack_ff(py[c], py[c + 1]));
+                                acc[1] = add_f32x2(acc[1], pack_ff(py[c + 2], py[c + 3]));
+                                pk[(16 * (i - 1) + c) / 2] = pack_f16x2(py[c], py[c + 1]);
+                                pk[(16 * (i - 1) + c) / 2 + 1] = pack_f16x2(py[c + 2], py[c + 3]);
+                            }
                         }
                     }
                     float s0, s1;
