@@ -165,7 +165,7 @@ __device__ int64_t plan_scan(int64_t v, int64_t *buf, int64_t *total) {   // exc
 template <int ROWS, int KT>
 __global__ void __launch_bounds__(kPlanThreads)
 k_prefill_plan(const PagedView pv, const PrefillArgs a) {
-    __shared__ int64_t buf[32];
+    __shared__ int64_t buf[32], place[kPlanThreads];
     pdl_wait();
     pdl_trigger();
     int64_t base = 0, all;
@@ -204,13 +204,23 @@ k_prefill_plan(const PagedView pv, const PrefillArgs a) {
         const int64_t i = i0 + threadIdx.x;
         if (nb > kPlanThreads || i >= nb) mine = tiles_at(i, &who);
         const int64_t pre = base + plan_scan(mine, buf, &all);
-        base += all;
-        if (i < nb) {
-            a.block[i] = who;
-            // the CTAs whose first place, total * c / n, lies here
-            for (int64_t c = (pre * n + total - 1) / total; c < n && total * c / n < pre + mine; ++c)
-                a.start[c] = make_longlong2(i, pre);
+        if (i < nb) a.block[i] = who;
+        // a thread per CTA: its first place, total * c / n, and the row block that holds it, if it is one of these
+        place[threadIdx.x] = pre;
+        __syncthreads();
+        const int blocks = (int)min((int64_t)kPlanThreads, nb - i0);
+        for (int64_t c = threadIdx.x; c < n; c += kPlanThreads) {
+            const int64_t at = total * c / n;
+            if (at < base || at >= base + all) continue;
+            int lo = 0, hi = blocks - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (place[mid] <= at) lo = mid; else hi = mid - 1;
+            }
+            a.start[c] = make_longlong2(i0 + lo, place[lo]);
         }
+        base += all;
+        __syncthreads();              // the next blocks' places go there
     }
 }
 
