@@ -685,9 +685,9 @@ def paged_kv_evict(k_cache, v_cache, block_table, seq_lens, mass, dst_table, bud
     _, db = _table_shape(dst_table, seq_lens, "dst_table")
     if mass.dim() != 3 or tuple(mass.shape[:2]) != (B, H):
         raise ValueError("expected mass [B, H, ld]")
-    kept = torch.empty((B, H, max(budget, 0)), dtype=torch.int32, device=mass.device)
-    mass_out = torch.empty_like(mass)
-    lens_out = torch.empty(B, dtype=torch.int32, device=mass.device)
+    kept = seq_lens.new_empty((B, H, max(budget, 0)))
+    mass_out = mass.new_empty(mass.shape)
+    lens_out = seq_lens.new_empty(B)
     fp8_paged_kv_evict(*caches, H, k_cache.Dh, bs, k_cache.num_blocks, block_table, seq_lens, B, mb, mass,
                        mass.shape[2], dst_table, db, budget, sinks, recent, kept, mass_out, mass.shape[2],
                        lens_out)

@@ -512,3 +512,72 @@ def test_a_token_leaves_the_batch_unchanged_for_the_others():
     q = inputs.normal_bf16((3, 4, 64), 1.0, seed=52).to(DEV)
     out, lse = fp8q.paged_attention_decode(q, k, v, table, ln)
     check_rows(out, lse, q, k, v, table, lens, [(b, b, n - 1) for b, n in enumerate(lens)], 0.125, 0, 0)
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+def test_more_sequences_than_threads(kind):
+    """1300 sequences of 0 to 40 tokens, one or two of them new (more row blocks than one pass of the planning
+    kernels takes), checked at the ends of the passes and in between."""
+    B, H, G, Dh, bs = 1300, 2, 2, 32, 8
+    lens = [(7 * b) % 41 for b in range(B)]
+    k, v, table, ln = make_caches(lens, H, Dh, bs, 0, seed=61)
+    new = [1] * B if kind == "decode" else [min(n, 1 + b % 2) for b, n in enumerate(lens)]
+    off = torch.tensor([0] + new).cumsum(0)
+    q = inputs.normal_bf16((int(off[-1]), H * G, Dh), 1.0, seed=62).to(DEV)
+    if kind == "decode":
+        out, lse = fp8q.paged_attention_decode(q, k, v, table, ln)
+    else:
+        out, lse = fp8q.paged_attention_prefill(q, off.to(DEV), k, v, table, ln)
+    some = sorted(set(range(0, B, 37)) | {511, 512, 513, 1022, 1023, 1024, 1025, B - 2, B - 1})
+    rows = [(int(off[b]) + i, b, lens[b] - new[b] + i) for b in some for i in range(new[b])]
+    check_rows(out, lse, q, k, v, table, lens, rows, Dh ** -0.5, 0, 0, scaled_v=kind == "prefill")
+
+
+@pytest.mark.parametrize("slope", [0.4, -0.4, 8.0])
+@pytest.mark.parametrize("Dh", [64, 256])
+def test_logits_that_rise_or_fall_along_the_sequence(slope, Dh):
+    """Every tile moves the softmax reference, by up to a thousand powers of two (or none after the first does)."""
+    n, bs = 700, 16
+    k, v, table, ln = make_caches([n], 1, Dh, bs, 0, seed=71)
+    _, slots = inputs.paged_layout([n], bs, k.num_blocks, 71)
+    u = torch.ones(Dh) / Dh ** 0.5
+    ramp = slope * (torch.arange(n, dtype=torch.float32) - n / 2)
+    noise = inputs.normal_bf16((n, 1, Dh), 0.5, seed=72).float()
+    k.write((ramp[:, None, None] * u + noise).bfloat16().to(DEV), slots.to(DEV))
+    new = 150
+    q = (u + inputs.normal_bf16((new, 3, Dh), 0.05, seed=73).float()).bfloat16().to(DEV)
+    out, lse = fp8q.paged_attention_prefill(q, torch.tensor([0, new], device=DEV), k, v, table, ln, softmax_scale=1.0)
+    rows = [(i, 0, n - new + i) for i in (0, 1, 31, 77, 127, 128, new - 1)]
+    check_rows(out, lse, q, k, v, table, [n], rows, 1.0, 0, 0, scaled_v=True)
+    out, lse = fp8q.paged_attention_decode(q[-1:], k, v, table, ln, softmax_scale=1.0)
+    check_rows(out, lse, q[-1:], k, v, table, [n], [(0, 0, n - 1)], 1.0, 0, 0)
+
+
+def test_two_calls_at_once():
+    """Decode and prefill side by side on two streams, each with its own workspace, give what they give alone; the
+    sequences share pages."""
+    lens = [3000, 2000, 2500]
+    H, G, Dh = 4, 2, 128
+    k, v, table, ln = make_caches(lens, H, Dh, 16, 0, seed=81)
+    table[1, :40] = table[0, :40]                        # a prefix in common
+    q = inputs.normal_bf16((3, H * G, Dh), 1.0, seed=82).to(DEV)
+    q2 = inputs.normal_bf16((600, H * G, Dh), 1.0, seed=83).to(DEV)
+    off = torch.tensor([0, 200, 400, 600], device=DEV)
+    ws = fp8q.paged_attention_workspace(3, H * G, H, Dh, table.shape[1] * 16)
+    wp = fp8q.paged_attention_workspace(3, H * G, H, Dh, tokens=600)
+    alone = [x.clone() for x in fp8q.paged_attention_decode(q, k, v, table, ln, workspace=ws)]
+    alone2 = [x.clone() for x in fp8q.paged_attention_prefill(q2, off, k, v, table, ln, workspace=wp)]
+    check_rows(*alone, q, k, v, table, lens, [(b, b, n - 1) for b, n in enumerate(lens)], Dh ** -0.5, 0, 0)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got, got2 = [], []
+    for _ in range(10):
+        with torch.cuda.stream(s1):
+            got.append(fp8q.paged_attention_decode(q, k, v, table, ln, workspace=ws))
+        with torch.cuda.stream(s2):
+            got2.append(fp8q.paged_attention_prefill(q2, off, k, v, table, ln, workspace=wp))
+    torch.cuda.synchronize()
+    for r, r2 in zip(got, got2):
+        assert torch.equal(r[0], alone[0]) and torch.equal(r[1], alone[1])
+        assert torch.equal(r2[0], alone2[0]) and torch.equal(r2[1], alone2[1])
+    assert fp8q.fp8_device_error() == 0
