@@ -32,6 +32,12 @@
 // writes its result; otherwise it leaves (O, max, sum) in the workspace and
 // k_decode_join adds the parts in the order of the CTAs.  At most two parts
 // per CTA, so the workspace does not grow with the batch.
+//
+// Measured on a B200 with L2 flushed: 32 sequences of up to 8192 tokens, 32
+// heads of 128, 1.12 GB in 190 us (5.9 TB/s, 0.91 of a copy); one of 131072
+// tokens, 8 heads with 8 query heads each, 277 MB in 59 us (55 of them in this
+// kernel, 12 of those before the first and after the last tile).  Tiles by TMA
+// instead of cp.async: 306 -> 235 us and 118 -> 97 us when they came in.
 #include <algorithm>
 #include <atomic>
 

@@ -17,6 +17,10 @@
 // that its writes are whole token rows; it looks the rows' slots up once, into
 // shared memory, and then copies 16 bytes per thread and load, eight loads in
 // flight.
+//
+// Measured on a B200 with L2 flushed: 16 sequences x 32 heads of 128, 8192
+// tokens to 4096: selection 47 us, copy 212 us (1.1 GB read and written, 5.4
+// TB/s).  Selection by 1024 threads instead of 512: 10 - 15 us slower there.
 #include <algorithm>
 
 #include "paged.cuh"

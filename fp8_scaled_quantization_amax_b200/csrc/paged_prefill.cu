@@ -31,6 +31,15 @@
 // leave (O, reference, sum) in the workspace and k_prefill_join adds the parts in
 // the order of the CTAs.
 //
+// Measured on a B200, 32 query heads over 8 KV heads of 128: 8192 tokens 660 -
+// 690 us (800 - 830 TFLOP/s), tensor pipe 40 % busy, MUFU 40 %, issue slots 47 %.
+// What bounds it is the chain of a row tile: softmax of 128 columns 2100 - 2600
+// cycles (128 exponentials of 8 cycles each and what they wait for), P to TMEM
+// 300, P V and the next S 1500 with their waits; two row tiles in turn take 4400 -
+// 5000 cycles where the tensor core needs 1024.  A unit costs 13000 - 17000
+// cycles more, for Q and the results.  Codes by TMA instead of cp.async: 1.01 ->
+// 0.97 ms when that came in.
+//
 // What a row must not see is kept out of it whatever it holds: S is masked by
 // selection; V rows of slots that are no live position are written as zeros;
 // and since a weight of zero does not hide a NaN or infinity in V, such values

@@ -583,7 +583,8 @@ FP8Q_API fp8_status fp8_paged_attention_decode(
  *             not written.
  *   out_bf16  [T, Hq, Dh] bf16, dense.  lse [T, Hq] fp32 or NULL.
  *   The remaining arguments, shapes, errors, determinism and the workspace are
- *   those of fp8_paged_attention_decode.  T * Hq < 2^31.
+ *   those of fp8_paged_attention_decode.  T * Hq < 2^31.  Here V's scales are
+ *   applied to V in fp16 (two roundings of 2^-11), not to P.
  */
 FP8Q_API fp8_status fp8_paged_attention_prefill(
     const void *q_bf16, int64_t ld_q, int64_t T, const int64_t *q_offsets, int64_t B, int64_t Hq,
