@@ -7,6 +7,8 @@
 namespace fp8q_host {
 
 constexpr int kAttnMaxDh = 256;
+// rows of q times query heads: row numbers, and the ends of the row blocks that hold them, stay below 2^31
+constexpr int64_t kAttnMaxRows = 0x7FFF0000ll;
 
 inline fp8_status attn_shape(int64_t ld_q, int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t Dh,
                              int64_t block_size, int64_t num_blocks, int64_t max_blocks, int64_t window,
@@ -14,7 +16,7 @@ inline fp8_status attn_shape(int64_t ld_q, int64_t T, int64_t B, int64_t Hq, int
     const fp8_status st = paged_cache_shape(H, Dh, block_size, num_blocks);
     if (st != FP8_OK) return st;
     if (Dh % 16 || Dh > kAttnMaxDh || Hq < 1 || Hq > 0x7FFFFFFFll || Hq % H) return FP8_ERR_SHAPE;
-    if (B < 0 || B > 65535 || T < 0 || T > 0x7FFFFFFFll || T * Hq > 0x7FFFFFFFll || max_blocks < 0 || window < 0 ||
+    if (B < 0 || B > 65535 || T < 0 || T > 0x7FFFFFFFll || T * Hq > kAttnMaxRows || max_blocks < 0 || window < 0 ||
         sinks < 0)
         return FP8_ERR_SHAPE;
     if (max_blocks > kPagedMaxContext / block_size || ld_q < Hq * Dh) return FP8_ERR_SHAPE;

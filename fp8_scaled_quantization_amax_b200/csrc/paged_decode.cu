@@ -955,6 +955,7 @@ extern "C" fp8_status fp8_paged_attention_decode(
     if (fmt != FP8_E4M3 && fmt != FP8_E5M2) return FP8_ERR_INVALID_ARG;
     fp8_status st = attn_shape(ld_q, B, B, Hq, H, Dh, block_size, num_blocks, max_blocks, window, sinks);
     if (st != FP8_OK) return st;
+    if (B * Hq * (Dh <= 64 ? 2 : Dh <= 128 ? 4 : 8) > 0x7FFFFFFFll) return FP8_ERR_SHAPE;   // the join's CTAs
     if (mass && ld_mass < 0) return FP8_ERR_SHAPE;
     if (!std::isfinite(softmax_scale) || (mass && !std::isfinite(mass_decay))) return FP8_ERR_INVALID_ARG;
     if (B == 0) return FP8_OK;

@@ -554,9 +554,9 @@ FP8Q_API fp8_status fp8_paged_kv_gather(const uint8_t *cache, const float *scale
  *   products with V are fp16 tensor-core products with fp32 sums; logits,
  *   maxima and sums are fp32.
  *   Shapes: Dh % 16 == 0, 16 <= Dh <= 256, H * Dh <= 8192, Hq % H == 0,
- *   B <= 65535, num_blocks * block_size < 2^31, max_blocks * block_size <=
- *   2^31 - 65536, window, sinks >= 0,
- *   softmax_scale and mass_decay finite.
+ *   B <= 65535, B * Hq * Dh (rounded up to 64, 128 or 256) < 2^36,
+ *   num_blocks * block_size < 2^31, max_blocks * block_size <= 2^31 - 65536,
+ *   window, sinks >= 0, softmax_scale and mass_decay finite.
  *   Errors: FP8_ERR_SHAPE, FP8_ERR_INVALID_ARG (NULL pointer, format, a
  *   workspace that is too small, a scale that is not finite),
  *   FP8_ERR_ALIGNMENT (q, out, the caches and the workspace 16 bytes, ld_q a
@@ -583,7 +583,7 @@ FP8Q_API fp8_status fp8_paged_attention_decode(
  *             not written.
  *   out_bf16  [T, Hq, Dh] bf16, dense.  lse [T, Hq] fp32 or NULL.
  *   The remaining arguments, shapes, errors, determinism and the workspace are
- *   those of fp8_paged_attention_decode.  T * Hq < 2^31.  Here V's scales are
+ *   those of fp8_paged_attention_decode.  T * Hq <= 2^31 - 65536.  Here V's scales are
  *   applied to V in fp16 (two roundings of 2^-11), not to P.
  */
 FP8Q_API fp8_status fp8_paged_attention_prefill(

@@ -65,6 +65,14 @@ def test_attention_refuses_what_is_its_own():
     assert decode(B=0) == OK and prefill(B=0) == OK and prefill(T=0) == OK
 
 
+def test_attention_refuses_more_rows_than_it_can_number():
+    """Row blocks of 256 rows have to end below 2^31, and decode's join takes a block per 32 elements of a row."""
+    assert prefill(T=(1 << 28) - 1) == SHAPE and prefill(T=1, Hq=(1 << 31) - 2, ld_q=BIG) == SHAPE
+    for Dh, Hq in ((64, 1 << 20), (80, 1 << 19), (128, 1 << 19), (256, 1 << 18)):
+        assert decode(B=1 << 10, Hq=Hq, Dh=Dh, ld_q=BIG) == SHAPE       # 2^31 blocks
+        assert decode(B=1 << 10, Hq=Hq - 2, Dh=Dh, ld_q=BIG, q=None) == INVALID
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(H=0), SHAPE), (dict(Dh=12), SHAPE), (dict(H=256), SHAPE), (dict(B=-1), SHAPE), (dict(B=65536), SHAPE),
     (dict(bs=0), SHAPE), (dict(nb=1 << 30), SHAPE), (dict(mb=-1), SHAPE), (dict(dmb=-1), SHAPE), (dict(mb=1 << 27), SHAPE), (dict(dmb=1 << 27), SHAPE),
