@@ -126,15 +126,12 @@ def _dev(t, dtype, what):
         raise ValueError(f"{what}: must be contiguous")
 
 
-def _fits(t, dtype, index):
-    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
-
-
 def _dev_on(index, checks):
     """_dev() for (tensor or None, dtype, name) triples, all on the CUDA device `index`: the library runs there,
     whatever the current device is."""
-    for t, dtype, what in checks:
-        if t is not None and not _fits(t, dtype, index):
+    for t, dtype, what in checks:                  # ten a call: written out, which saves a microsecond
+        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+                                  and t.is_contiguous()):
             _dev(t, dtype, what)
             raise ValueError(f"{what}: on {t.device}, expected cuda:{index}")
 
@@ -412,10 +409,18 @@ def fp8_paged_attention_decode(q, ld_q, B, Hq, k_cache, k_scale, v_cache, v_scal
     _dev_on(d, ((k_cache, u8, "k_cache"), (v_cache, u8, "v_cache"), (k_scale, f32, "k_scale"),
                 (v_scale, f32, "v_scale"), (block_table, i32, "block_table"), (seq_lens, i32, "seq_lens"),
                 (out, torch.bfloat16, "out"), (lse, f32, "lse"), (mass, f32, "mass"), (workspace, u8, "workspace")))
+    _decode_call(d, stream, q, ld_q, B, Hq, (k_cache, k_scale, v_cache, v_scale), (H, Dh, block_size, num_blocks, fmt),
+                 block_table, seq_lens, max_blocks, window, sinks, softmax_scale, out, lse, mass, ld_mass, mass_decay,
+                 workspace)
+
+
+def _decode_call(d, stream, q, ld_q, B, Hq, caches, shape, block_table, seq_lens, max_blocks, window, sinks,
+                 softmax_scale, out, lse, mass, ld_mass, mass_decay, workspace):
+    """Checked tensors on device d; shape: (H, Dh, block_size, num_blocks, fmt)."""
     _call_on(d, "fp8_paged_attention_decode", stream, (
-        _addr(q), ld_q, B, Hq, _addr(k_cache), _addr(k_scale), _addr(v_cache), _addr(v_scale), H, Dh, block_size,
-        num_blocks, fmt, _addr(block_table), _addr(seq_lens), max_blocks, window, sinks, softmax_scale, _addr(out),
-        _addr(lse), _addr(mass), ld_mass, mass_decay, _addr(workspace), 0 if workspace is None else workspace.numel()))
+        q.data_ptr(), ld_q, B, Hq, *map(_addr, caches), *shape, _addr(block_table), _addr(seq_lens), max_blocks, window,
+        sinks, softmax_scale, _addr(out), _addr(lse), _addr(mass), ld_mass, mass_decay, _addr(workspace),
+        0 if workspace is None else workspace.numel()))
 
 
 def fp8_paged_attention_prefill(q, ld_q, T, q_offsets, B, Hq, k_cache, k_scale, v_cache, v_scale, H, Dh, block_size,
@@ -427,10 +432,18 @@ def fp8_paged_attention_prefill(q, ld_q, T, q_offsets, B, Hq, k_cache, k_scale, 
                 (v_scale, f32, "v_scale"), (q_offsets, torch.int64, "q_offsets"), (block_table, i32, "block_table"),
                 (seq_lens, i32, "seq_lens"), (out, torch.bfloat16, "out"), (lse, f32, "lse"),
                 (workspace, u8, "workspace")))
+    _prefill_call(d, stream, q, ld_q, T, q_offsets, B, Hq, (k_cache, k_scale, v_cache, v_scale),
+                  (H, Dh, block_size, num_blocks, fmt), block_table, seq_lens, max_blocks, window, sinks, softmax_scale,
+                  out, lse, workspace)
+
+
+def _prefill_call(d, stream, q, ld_q, T, q_offsets, B, Hq, caches, shape, block_table, seq_lens, max_blocks, window,
+                  sinks, softmax_scale, out, lse, workspace):
+    """Checked tensors on device d; shape: (H, Dh, block_size, num_blocks, fmt)."""
     _call_on(d, "fp8_paged_attention_prefill", stream, (
-        _addr(q), ld_q, T, _addr(q_offsets), B, Hq, _addr(k_cache), _addr(k_scale), _addr(v_cache), _addr(v_scale), H,
-        Dh, block_size, num_blocks, fmt, _addr(block_table), _addr(seq_lens), max_blocks, window, sinks, softmax_scale,
-        _addr(out), _addr(lse), _addr(workspace), 0 if workspace is None else workspace.numel()))
+        q.data_ptr(), ld_q, T, _addr(q_offsets), B, Hq, *map(_addr, caches), *shape, _addr(block_table),
+        _addr(seq_lens), max_blocks, window, sinks, softmax_scale, _addr(out), _addr(lse), _addr(workspace),
+        0 if workspace is None else workspace.numel()))
 
 
 def fp8_paged_attention_workspace_size(B, Hq, H, Dh, max_context, weights, tokens) -> int:
@@ -607,6 +620,11 @@ def _kv_pair(k_cache, v_cache):
     return (k_cache.cache, k_cache.scale_inv, v_cache.cache, v_cache.scale_inv)
 
 
+def _cache_checks(caches):
+    return ((caches[0], torch.uint8, "k_cache"), (caches[1], torch.float32, "k_scale"),
+            (caches[2], torch.uint8, "v_cache"), (caches[3], torch.float32, "v_scale"))
+
+
 def _table_shape(block_table, seq_lens, what="block_table"):
     if block_table.dim() != 2 or seq_lens.dim() != 1 or block_table.shape[0] != seq_lens.shape[0]:
         raise ValueError(f"expected {what} [B, max_blocks] and seq_lens [B]")
@@ -627,7 +645,7 @@ def paged_attention_decode(q, k_cache, v_cache, block_table, seq_lens, window=0,
     paged caches (PagedKVCache of K and of V).  window > 0: only the last `window` positions and the first `sinks`.
     mass [B, H, ld] fp32: becomes mass_decay * mass + each visible token's attention weight, summed over the query
     heads of its KV head.  softmax_scale: Dh ** -0.5 unless given."""
-    _, ld_q = _token_rows(q, "q")
+    d, ld_q = _token_rows(q, "q")
     B, Hq, Dh = q.shape
     caches = _kv_pair(k_cache, v_cache)
     H = k_cache.H
@@ -642,10 +660,11 @@ def paged_attention_decode(q, k_cache, v_cache, block_table, seq_lens, window=0,
     lse = q.new_empty((B, Hq), dtype=torch.float32)
     if workspace is None and B:
         workspace = paged_attention_workspace(B, Hq, H, Dh, mb * k_cache.block_size, mass is not None, 0, q.device)
-    fp8_paged_attention_decode(q, ld_q, B, Hq, *caches, H, Dh, k_cache.block_size, k_cache.num_blocks, k_cache.fmt,
-                               block_table, seq_lens, mb, window, sinks,
-                               Dh ** -0.5 if softmax_scale is None else softmax_scale, o, lse, mass,
-                               0 if mass is None else mass.shape[2], mass_decay, workspace)
+    _dev_on(d, (*_cache_checks(caches), (block_table, torch.int32, "block_table"), (seq_lens, torch.int32, "seq_lens"),
+                (out, torch.bfloat16, "out"), (mass, torch.float32, "mass"), (workspace, torch.uint8, "workspace")))
+    _decode_call(d, None, q, ld_q, B, Hq, caches, (H, Dh, k_cache.block_size, k_cache.num_blocks, k_cache.fmt),
+                 block_table, seq_lens, mb, window, sinks, Dh ** -0.5 if softmax_scale is None else softmax_scale, o, lse,
+                 mass, 0 if mass is None else mass.shape[2], mass_decay, workspace)
     return o, lse
 
 
@@ -654,7 +673,7 @@ def paged_attention_prefill(q, q_offsets, k_cache, v_cache, block_table, seq_len
     """(out [T, Hq, Dh] bf16, lse [T, Hq] fp32): causal attention of the rows q_offsets[b] .. q_offsets[b + 1]
     (int64 [B + 1], device) of q [T, Hq, Dh], the last positions of sequence b, over the paged caches.  Rows that
     belong to no sequence are not written."""
-    _, ld_q = _token_rows(q, "q")
+    d, ld_q = _token_rows(q, "q")
     T, Hq, Dh = q.shape
     caches = _kv_pair(k_cache, v_cache)
     H = k_cache.H
@@ -669,9 +688,12 @@ def paged_attention_prefill(q, q_offsets, k_cache, v_cache, block_table, seq_len
     lse = q.new_empty((T, Hq), dtype=torch.float32)
     if workspace is None and T:
         workspace = paged_attention_workspace(B, Hq, H, Dh, tokens=T, device=q.device)
-    fp8_paged_attention_prefill(q, ld_q, T, q_offsets, B, Hq, *caches, H, Dh, k_cache.block_size, k_cache.num_blocks,
-                                k_cache.fmt, block_table, seq_lens, mb, window, sinks,
-                                Dh ** -0.5 if softmax_scale is None else softmax_scale, o, lse, workspace)
+    _dev_on(d, (*_cache_checks(caches), (q_offsets, torch.int64, "q_offsets"), (block_table, torch.int32, "block_table"),
+                (seq_lens, torch.int32, "seq_lens"), (out, torch.bfloat16, "out"),
+                (workspace, torch.uint8, "workspace")))
+    _prefill_call(d, None, q, ld_q, T, q_offsets, B, Hq, caches,
+                  (H, Dh, k_cache.block_size, k_cache.num_blocks, k_cache.fmt), block_table, seq_lens, mb, window, sinks,
+                  Dh ** -0.5 if softmax_scale is None else softmax_scale, o, lse, workspace)
     return o, lse
 
 
