@@ -581,3 +581,70 @@ def test_two_calls_at_once():
         assert torch.equal(r[0], alone[0]) and torch.equal(r[1], alone[1])
         assert torch.equal(r2[0], alone2[0]) and torch.equal(r2[1], alone2[1])
     assert fp8q.fp8_device_error() == 0
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+def test_softmax_scales_of_zero_and_below(scale):
+    """Zero weighs all visible tokens alike; a negative scale turns the order round."""
+    lens, new, Dh = [333, 20], [40, 20], 128
+    k, v, table, ln = make_caches(lens, 2, Dh, 16, 0, seed=91)
+    off = torch.tensor([0, 40, 60])
+    q = inputs.normal_bf16((60, 6, Dh), 1.0, seed=92).to(DEV)
+    s = float(torch.tensor(scale))                       # as the call takes it: fp32
+    out, lse = fp8q.paged_attention_prefill(q, off.to(DEV), k, v, table, ln, 100, 3, softmax_scale=scale)
+    rows = [(int(off[b]) + i, b, lens[b] - new[b] + i) for b in range(2) for i in (0, 7, new[b] - 1)]
+    check_rows(out, lse, q, k, v, table, lens, rows, s, 100, 3, scaled_v=True)
+    out, lse = fp8q.paged_attention_decode(q[:2], k, v, table, ln, 100, 3, softmax_scale=scale)
+    check_rows(out, lse, q, k, v, table, lens, [(b, b, n - 1) for b, n in enumerate(lens)], s, 100, 3)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_query_that_is_not_finite_stays_in_its_row(bad):
+    lens, new = [200, 150], 100
+    k, v, table, ln = make_caches(lens, 2, 64, 16, 0, seed=95)
+    off = torch.tensor([0, new, 2 * new], device=DEV)
+    q = inputs.normal_bf16((2 * new, 4, 64), 1.0, seed=96).to(DEV)
+    q2 = q.clone()
+    q2[17, 1, 5] = bad
+    out, lse = fp8q.paged_attention_prefill(q, off, k, v, table, ln)
+    o2, l2 = fp8q.paged_attention_prefill(q2, off, k, v, table, ln)
+    assert not torch.isfinite(l2[17, 1]) and not torch.isfinite(o2[17, 1].float()).all()
+    hit = torch.zeros(2 * new, 4, dtype=torch.bool, device=DEV)
+    hit[17, 1] = True
+    assert torch.equal(o2[~hit], out[~hit]) and torch.equal(l2[~hit], lse[~hit])
+    out, lse = fp8q.paged_attention_decode(q[16:18], k, v, table, ln)
+    o2, l2 = fp8q.paged_attention_decode(q2[16:18], k, v, table, ln)
+    assert not torch.isfinite(l2[1, 1]) and not torch.isfinite(o2[1, 1].float()).all()
+    assert torch.equal(o2[~hit[16:18]], out[~hit[16:18]]) and torch.equal(l2[~hit[16:18]], lse[~hit[16:18]])
+
+
+@pytest.mark.parametrize("bs", [64, 7])
+def test_a_pool_past_four_gigabytes(bs):
+    """Pages whose bytes lie behind 2^32 give what the same pages give in a small pool, bit for bit."""
+    lens, H, Dh = [200, 91], 8, 256
+    k, v, table, ln = make_caches(lens, H, Dh, bs, 0, seed=97, spare=40)
+    nb = 2200000 // bs
+    assert nb * bs * H * Dh > 1 << 32
+    K, V = (fp8q.PagedKVCache(nb, bs, H, Dh, 0, device=DEV) for _ in range(2))
+    shift = nb - k.num_blocks
+    for big, small in ((K, k), (V, v)):
+        big.cache[shift:] = small.cache
+        big.scale_inv[shift:] = small.scale_inv
+    far = torch.where(table >= 0, table + shift, table)
+    q = inputs.normal_bf16((60, 16, Dh), 1.0, seed=98).to(DEV)
+    off = torch.tensor([0, 40, 60], device=DEV)
+    mass, mass2 = (torch.zeros((2, H, 200), device=DEV) for _ in range(2))
+    got = [fp8q.paged_attention_decode(q[:2], *c, t, ln, mass=m) + fp8q.paged_attention_prefill(q, off, *c, t, ln)
+           for c, t, m in (((k, v), table, mass), ((K, V), far, mass2))]
+    assert all(torch.equal(x, y) for x, y in zip(*got)) and torch.equal(mass, mass2)
+    used = {int(x) for x in table.flatten()}
+    free = [x for x in range(k.num_blocks) if x not in used]
+    n = (50 + bs - 1) // bs
+    dst = torch.tensor([free[:n], free[n:2 * n]], dtype=torch.int32, device=DEV)
+    a = fp8q.paged_kv_evict(k, v, table, ln, mass, dst, 50, 2, 10)
+    b = fp8q.paged_kv_evict(K, V, far, ln, mass2, dst + shift, 50, 2, 10)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    for big, small in ((K, k), (V, v)):
+        assert torch.equal(big.cache[shift:], small.cache)
+        assert torch.equal(big.scale_inv[shift:].nan_to_num(7.0), small.scale_inv.nan_to_num(7.0))
+        assert not big.cache[:1000].any()
