@@ -738,7 +738,9 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 uint32_t all = 0xFFFFFFFFu;
 #pragma unroll
                 for (int e = 0; e < KT / 32; ++e) all &= ld_shared_u32(meta(kc) + P::M_LIVE + 4 * e);
-                const bool part = all != 0xFFFFFFFFu || !tile_full<KT>(pv, run.u, tile_pos<KT>(run.u, run.tile + k));
+                // what is taken out of V here is what the results add again: tiles that some rows do not see, whether or
+                // not pages are missing
+                const bool dead = all != 0xFFFFFFFFu, part = !tile_full<KT>(pv, run.u, tile_pos<KT>(run.u, run.tile + k));
 #pragma unroll 1
                 for (uint32_t i = 2 * kc; i < 2 * kc + 2; ++i) {
                     const bool is_v = i & 1;
@@ -760,7 +762,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 f[e] = __uint_as_float(ld_shared_u32(dv + (e0 + e) * 16 * RPI)) * fp;
-                            if (part) {
+                            if (dead || part) {
                                 // slots that are no live position are zeros, and what only some rows see must be finite
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
@@ -768,6 +770,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                                     const bool live =
                                         (ld_shared_u32(meta(kc) + P::M_LIVE + 4 * (r >> 5)) >> (r & 31)) & 1u;
                                     if (!live) q[e] = make_uint4(0, 0, 0, 0);
+                                    if (!part) continue;
                                     const uint32_t nf = nonfinite4<FMT>(q[e].x) | nonfinite4<FMT>(q[e].y) |
                                                         nonfinite4<FMT>(q[e].z) | nonfinite4<FMT>(q[e].w);
                                     if (nf || !(fabsf(f[e]) < INFINITY)) {
