@@ -12,7 +12,9 @@
 // of S in fp32 (in the multiply-add that subtracts the reference); V's are
 // multiplied into the fp16 V (rounded to fp16 as a factor and as a product,
 // 2^-11 each: in P they would cost a multiply and a shared load per weight),
-// against a running power of two of the largest scale so far.  Q is brought to
+// against a running power of two of the largest scale so far.  Where the scales
+// of a run are too far apart for that, V is the codes and the scales multiply P,
+// each row by a power of two of its own.  Q is brought to
 // [2^14, 2^15) by a power of two.  The softmax reference is set to 2^7 below a
 // maximum and only moves when a tile's weights sum to 2^15, so neither the
 // maximum of a tile is looked for nor O rescaled but seldom, and weights are
@@ -90,13 +92,20 @@ struct Pre {
     static constexpr int META = 8;                        // tiles whose scales and masks are kept
     static constexpr int OFF_KV = MT * QB, OFF_RAW = OFF_KV + RING * KVB, OFF_M = OFF_RAW + RING * RAW;
     static constexpr int M_DK = 0, M_DV = KT * 4, M_SLOT = KT * 8, M_LIVE = KT * 12, M_MAX = M_LIVE + 16,
-                         M_EXP = M_MAX + 16, M_BYTES = M_EXP + 16;
+                         M_MIN = M_MAX + 4, M_EXP = M_MAX + 8, M_BYTES = M_MAX + 16;
     static constexpr int OFF_BAR = OFF_M + META * M_BYTES;
     static constexpr int NBARS = 4 * RING + 4 * MT + 1 + META;
     static constexpr size_t SMEM = 1024 + OFF_BAR + NBARS * 8;
     static constexpr int S_COL = KT, O_COL = 256;         // TMEM: S of tile i at i * S_COL, O at O_COL + i * DH
     static constexpr int VC_E4M3 = 6, VC_E5M2 = -1;       // code * scale * 2^(VC - exponent of the largest) < 2^16
+    // V holds its scales while the exponents of a run's stay this close together.  E4M3: the factor is then 2^(6 - 11)
+    // or more and its product with the smallest code 2^-14, fp16's smallest normal.  E5M2 (codes down to 2^-16): the
+    // product is off by 2^-25 at most, 2^-16 of its own scale.  A weight below 2^-14 is off by 2^-25 too, which large
+    // scales must not make count.
+    static constexpr int SPREAD_E4M3 = 11, SPREAD_E5M2 = 8;
 };
+constexpr int kNoScale = -1000;       // exponent of V's scales, and of O's unit, before the first scale: O is zero
+constexpr int kWide = 0x40000000;     // in place of a tile's unit: the scales multiply the weights instead
 
 constexpr int kThreads = 512;
 // registers per thread: launch pool 128 * 512; MMA warpgroup, softmax, converter
@@ -406,6 +415,15 @@ __device__ __forceinline__ void tmem_ld16_async(uint32_t addr, uint32_t *o) {
           "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
         : "r"(addr));
 }
+__device__ __forceinline__ void tmem_ld8_async(uint32_t addr, uint32_t *o) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // waits for the loads in flight; the registers of this array cannot be read above it
 template <int N>
@@ -687,19 +705,23 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                         dk[i] = s[i] >= 0 ? pv.ks[(int64_t)s[i] * pv.H + h] : 0.0f;
                         dv[i] = s[i] >= 0 ? pv.vs[(int64_t)s[i] * pv.H + h] : 0.0f;
                     }
+                    uint32_t mx = 0, mn = 0xFFFFFFFFu;        // of the finite scales; of those that are not zero
 #pragma unroll
                     for (int i = 0; i < KT / 32; ++i) {
                         reinterpret_cast<float *>(m + P::M_DK)[32 * i + lane] = dk[i] * fabsf(a.scale) * kLog2e;
                         reinterpret_cast<float *>(m + P::M_DV)[32 * i + lane] = dv[i];
                         reinterpret_cast<int *>(m + P::M_SLOT)[32 * i + lane] = s[i];
                         const uint32_t live = __ballot_sync(0xFFFFFFFFu, s[i] >= 0);
-                        const float d = fabsf(dv[i]);
-                        const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, d < INFINITY ? __float_as_uint(d) : 0u);
-                        if (lane == 0) {
-                            reinterpret_cast<uint32_t *>(m + P::M_LIVE)[i] = live;
-                            reinterpret_cast<uint32_t *>(m + P::M_MAX)[i] = mx;
+                        const uint32_t d = __float_as_uint(fabsf(dv[i]));
+                        if (d < 0x7F800000u) {
+                            mx = max(mx, d);
+                            if (d) mn = min(mn, d);
                         }
+                        if (lane == 0) reinterpret_cast<uint32_t *>(m + P::M_LIVE)[i] = live;
                     }
+                    mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+                    mn = __reduce_min_sync(0xFFFFFFFFu, mn);
+                    if (lane == 0) *reinterpret_cast<uint2 *>(m + P::M_MAX) = make_uint2(mx, mn);
                     arrive_release(mfull(kc));
                 }
             }
@@ -712,17 +734,25 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         const int tid = threadIdx.x - 384, c = lane % CH, r0 = (tid >> 5) * RPI + lane / CH;
         const int swap = (c >> 2) & 1;        // half the chunks are stored high half first: no bank conflicts
         uint32_t kc = 0;
-        int ex = -1000;                       // exponent of the largest V scale of the run so far
+        int ex = kNoScale;                    // exponent of the largest V scale of the run so far
+        uint32_t least = 0xFFFFFFFFu;         // and the smallest of them
+        bool wide = false;                    // from the first tile on that has them too far apart: V is the codes
+        constexpr int VC = FMT == FP8_E4M3 ? P::VC_E4M3 : P::VC_E5M2;
+        constexpr int SPREAD = FMT == FP8_E4M3 ? P::SPREAD_E4M3 : P::SPREAD_E5M2;
         auto meta = [&](uint32_t k) -> uint32_t { return sb + P::OFF_M + (k % P::META) * P::M_BYTES; };
         // waits for the slots of the k-th tile; the exponent its V is held against
         auto look_up = [&](uint32_t k, bool fresh) {
             wait_for(mfull(k), (k / P::META) & 1u, abort_flag, kErrProducer);
-            uint32_t mx = 0;
-#pragma unroll
-            for (int i = 0; i < KT / 32; ++i) mx = max(mx, ld_shared_u32(meta(k) + P::M_MAX + 4 * i));
-            if (fresh) ex = -1000;
-            if (mx) ex = max(ex, max((int)(mx >> 23) - 127, -100));
-            if (tid == 0) st_shared_u32(meta(k) + P::M_EXP, (uint32_t)ex);
+            const uint32_t mx = ld_shared_u32(meta(k) + P::M_MAX);
+            if (fresh) {
+                ex = kNoScale;
+                least = 0xFFFFFFFFu;
+                wide = false;
+            }
+            if (mx) ex = max(ex, max((int)(mx >> 23) - 127, -120));
+            least = min(least, ld_shared_u32(meta(k) + P::M_MIN));
+            wide |= (int)(least >> 23) - 127 < ex - SPREAD || ex > 125;   // 2^(VC - ex) is a float for -120 .. 125
+            if (tid == 0) st_shared_u32(meta(k) + P::M_EXP, (uint32_t)(wide ? kWide : ex > kNoScale ? ex - VC : ex));
         };
         auto put = [&](uint32_t base, int row, const uint32_t (&x)[8]) {
             const uint32_t at_row = base + (c >> 2) * (KT * 128) + row * 128, ch = (c & 3) * 2;
@@ -733,7 +763,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         for (; run.live(); run.next()) {
             for (int k = 0; k < run.len; ++k, ++kc) {
                 look_up(kc, k == 0);
-                const float fp = ex > -1000 ? pow2i(max((FMT == FP8_E4M3 ? P::VC_E4M3 : P::VC_E5M2) - ex, -126)) : 0.0f;
+                const float fp = wide ? 1.0f : ex > kNoScale ? pow2i(VC - ex) : 0.0f;
                 const uint32_t dv = meta(kc) + P::M_DV + 4 * r0;
                 uint32_t all = 0xFFFFFFFFu;
 #pragma unroll
@@ -781,6 +811,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                                     }
                                 }
                             }
+                            if (wide) f[0] = f[1] = f[2] = f[3] = 1.0f;
                         }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -814,6 +845,20 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbar.red.or.pred q, %1, 128, p;\n\t"
                 "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"(2 + mi), "r"((uint32_t)x) : "memory");
             return r != 0;
+        };
+        // S times f(column); rare, so eight columns of code
+        auto scale_s = [&](auto f) {
+#pragma unroll 1
+            for (int c = 0; c < KT; c += 8) {
+                uint32_t x[8];
+                tmem_ld8_async(ts + c, x);
+                tmem_ld_wait(x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f(c + i));
+                tmem_st4(ts + c, x[0], x[1], x[2], x[3]);
+                tmem_st4(ts + c + 4, x[4], x[5], x[6], x[7]);
+            }
+            tmem_st_wait();
         };
         uint32_t kc = 0, sc = 0;              // tiles of the CTA; S tiles of this row tile
         // the rows of this row tile in the run; Q as fp16
@@ -894,7 +939,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             const Unit u = run.u;
             const int tile = run.tile, len = run.len;
             float mr = kNoMax, l = 0.0f;
-            int ex = -1000;
+            int eo = kNoScale;                // O is in units of 2^eo
             for (int k = 0; k < len; ++k, ++kc, ++sc) {
                 const uint32_t m = sb + P::OFF_M + (kc % P::META) * P::M_BYTES;
                 const uint32_t fk = smem_u32(s_factor[mi][kc & 1]);
@@ -924,13 +969,17 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 // weights against the reference they find, and their sum tells afterwards whether one may have passed
                 // 2^15: P waits in registers (S's columns become P's), and such a tile is done again.
                 uint32_t pk[KT / 2];
-                float al = 1.0f, sum = 0.0f;
+                float dm = 0.0f, sum = 0.0f;  // the old reference less the new one
                 bool again = k == 0, bad = again, hide = masked;
+                if (odd_column)
+                    scale_s([&](int c) {
+                        const float o = __uint_as_float(ld_shared_u32(m + P::M_DK + 4 * c)) * qf;
+                        return o > 0.0f && o < INFINITY ? 1.0f : o;
+                    });
                 while (true) {
                     const bool raise = __any_sync(0xFFFFFFFFu, bad);
                     if (hide || raise) {
-                        // The maximum; and into S, -inf for what the row does not see and the product where the
-                        // column's factor is odd, so that the sweep needs no mask.
+                        // The maximum; and into S, -inf for what the row does not see, so that the sweep needs no mask.
                         float top = -INFINITY;
 #pragma unroll 1
                         for (int i = 0; i < KT / 32; ++i) {
@@ -941,13 +990,6 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                             tmem_ld32_async(ts + 32 * i, x);
                             tmem_ld_wait(x);
                             if (hide) {
-                                if (odd_column) {
-#pragma unroll
-                                    for (int c = 0; c < 32; ++c) {
-                                        const float o = __uint_as_float(ld_shared_u32(m + P::M_DK + 4 * (32 * i + c))) * qf;
-                                        if (!(o > 0.0f && o < INFINITY)) x[c] = __float_as_uint(__uint_as_float(x[c]) * o);
-                                    }
-                                }
 #pragma unroll
                                 for (int c = 0; c < 32; ++c)
                                     if (!((see >> c) & 1u)) x[c] = 0xFF800000u;   // -inf
@@ -964,7 +1006,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                         }
                         if (hide) tmem_st_wait();
                         if (bad && top > kNoMax) {
-                            al = exp2_fast(mr - (top - kBelow));
+                            dm = mr - (top - kBelow);
                             mr = top - kBelow;
                         }
                         again |= raise;
@@ -1008,11 +1050,9 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                     bad = !(sum < kMaxSum);
                     if (again || !__any_sync(0xFFFFFFFFu, bad)) break;   // a second NaN or infinity is the result
                 }
-                l = l * al + sum;
-                // ---- O against the new reference and V's exponent
-                const int ex_new = (int)ld_shared_u32(m + P::M_EXP);
-                if (k > 0 && (__any_sync(0xFFFFFFFFu, al != 1.0f) || ex_new != ex)) {
-                    if (ex_new != ex) al *= ex > -1000 && ex - ex_new >= -126 ? pow2i(ex - ex_new) : 0.0f;
+                // ---- O against the new reference and exponent; P over S's columns
+                const int unit = (int)ld_shared_u32(m + P::M_EXP);
+                auto rescale = [&](float al) {
                     wait_for(pvdone(mi), (sc - 1) & 1u, abort_flag, kErrEpilogue);
                     tc_fence_after();
 #pragma unroll 1
@@ -1024,11 +1064,54 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                         for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
                         tmem_st16(to + c, o);
                     }
-                }
-                ex = ex_new;
-                // ---- P over S's columns
+                };
+                if (unit != kWide) {
+                    if (__any_sync(0xFFFFFFFFu, dm != 0.0f || unit != eo)) {
+                        l *= exp2_fast(dm);
+                        if (k > 0) rescale(exp2_fast(dm + (float)(eo - unit)));
+                        eo = unit;
+                    }
+                    l += sum;
 #pragma unroll
-                for (int i = 0; i < KT / 32; ++i) tmem_st16(ts + 16 * i, pk + 16 * i);
+                    for (int i = 0; i < KT / 32; ++i) tmem_st16(ts + 16 * i, pk + 16 * i);
+                } else {
+                    // V's scales are far apart: they multiply the weights, and every row brings its products to
+                    // [2^13, 2^14) by a power of two of its own, so that a scale which it does not see, or hardly
+                    // weighs, costs it nothing.  Twice over the columns, eight at a time: the largest product (times
+                    // 2^-16, which keeps it finite), then P.
+                    const bool full = tile_full<KT>(pv, u, j0);      // otherwise scales that are none come with the result
+                    float top = 0.0f, g = 0.0f;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < 2 * KT; c0 += 8) {
+                        const int cc = c0 & (KT - 1);
+                        uint32_t x[8];
+                        float y[8];
+                        tmem_ld8_async(ts + cc, x);
+                        tmem_ld_wait(x);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            float d = __uint_as_float(ld_shared_u32(m + P::M_DV + 4 * (cc + c))) * 0x1p-16f;
+                            if (!full && !(fabsf(d) < INFINITY)) d = 0.0f;
+                            y[c] = exp2_fast(fmaf(__uint_as_float(x[c]), __uint_as_float(ld_shared_u32(fk + 4 * (cc + c))), -mr)) * d;
+                        }
+                        if (c0 < KT) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(y[c]) < INFINITY ? fabsf(y[c]) : 0.0f);
+                            if (cc < KT - 8) continue;
+                            // what O holds has shrunk by 2^dm; whole steps, within one of that however often it does
+                            int eo_new = eo - (int)fminf(floorf(mr) - floorf(mr + dm), 2000.0f);
+                            if (top > 0.0f) eo_new = max(eo_new, max((int)(__float_as_uint(top) >> 23) - 127, -113) + 3);
+                            const float al = exp2_fast(dm + (float)(eo - eo_new));
+                            if (k > 0 && __any_sync(0xFFFFFFFFu, al != 1.0f)) rescale(al);
+                            l = l * exp2_fast(dm) + sum;
+                            eo = eo_new;
+                            g = eo >= -110 ? pow2i(16 - eo) : 0.0f;
+                        } else {                      // P's columns lie behind those still to be read
+                            tmem_st4(ts + cc / 2, pack_f16x2(y[0] * g, y[1] * g), pack_f16x2(y[2] * g, y[3] * g),
+                                     pack_f16x2(y[4] * g, y[5] * g), pack_f16x2(y[6] * g, y[7] * g));
+                        }
+                    }
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 arrive_release(pfull(mi));
@@ -1045,25 +1128,25 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             // ---- this run's result
             wait_for(pvdone(mi), (sc - 1) & 1u, abort_flag, kErrEpilogue);
             tc_fence_after();
-            constexpr int vc = FMT == FP8_E4M3 ? P::VC_E4M3 : P::VC_E5M2;
-            const float fo = ex > -1000 ? pow2i(min(ex - vc, 127)) : 0.0f;
-            const float r = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f, by = fo * r;   // a weighted mean's scale: no overflow
+            // 2^eo in two steps: it may be more than a float, and a weighted mean less
+            const int e0 = max(eo >> 1, -126), e1 = max(eo - (eo >> 1), -126);
+            const float r = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+            float by = r * pow2i(e0) * pow2i(e1);
             float *part = a.part + ((int64_t)blockIdx.x * 2 + (tile == 0 ? 1 : 0)) * ((int64_t)ROWS * (DH + 2));
-            const bool poison = *reinterpret_cast<volatile uint32_t *>(&s_poison) != 0u;
+            if (*reinterpret_cast<volatile uint32_t *>(&s_poison) != 0u) {
+                // values that were taken out of V, all infinite or NaN: back into the rows that see them
 #pragma unroll 1
-            for (int c = 0; c < DH; c += 32) {
-                uint32_t o[32];
-                tmem_ld32_async(to + c, o);
-                tmem_ld_wait(o);
-                float v[32];
+                for (int c = 0; c < DH; c += 8) {
+                    uint32_t o[8];
+                    tmem_ld8_async(to + c, o);
+                    tmem_ld_wait(o);
+                    if (by == 0.0f)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * by;
-                if (poison) {
-                    // values that were taken out of V: back into the rows that see them
+                        for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
 #pragma unroll 1
                     for (int k = 0; k < len; ++k) {
                         const int j0 = tile_pos<KT>(u, tile + k);
-                        if (tile_full<KT>(pv, u, j0)) continue;
+                        if (c >= pv.Dh || tile_full<KT>(pv, u, j0)) continue;
 #pragma unroll 1
                         for (int j = j0; j < j0 + KT; ++j) {
                             if (j > p_was || !(j >= wb_was || j < pv.sinks)) continue;
@@ -1072,14 +1155,27 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                             const float d = pv.vs[(int64_t)s * pv.H + h_was];
                             const uint8_t *codes = pv.vc + (uint64_t)(uint32_t)s * (uint64_t)(pv.H * pv.Dh) + h_was * pv.Dh + c;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c + i < pv.Dh) {
-                                    const float w = fp8x2_to_float2<FMT>((uint16_t)codes[i]).x * d;
-                                    if (!(fabsf(w) < INFINITY)) v[i] += w;
-                                }
+                            for (int i = 0; i < 8; ++i) {
+                                const float w = fp8x2_to_float2<FMT>((uint16_t)codes[i]).x * d;
+                                if (!(fabsf(w) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + w);
+                            }
                         }
                     }
+                    __syncwarp();
+                    tmem_st4(to + c, o[0], o[1], o[2], o[3]);
+                    tmem_st4(to + c + 4, o[4], o[5], o[6], o[7]);
                 }
+                tmem_st_wait();
+                if (by == 0.0f) by = 1.0f;        // nothing finite is left; an infinity stays one
+            }
+#pragma unroll 1
+            for (int c = 0; c < DH; c += 32) {
+                uint32_t o[32];
+                tmem_ld32_async(to + c, o);
+                tmem_ld_wait(o);
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * by;
                 if (!valid_was || c >= pv.Dh) continue;
                 if (whole) {
                     __nv_bfloat16 *op = a.out + orow_was * pv.Dh + c;

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from fp8_scaled_quantization_amax_b200 import fp8q, inputs
+from tests import paged_bounds as bounds
 from tests.test_gpu_paged_attention import DEV, make_caches
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +47,127 @@ def test_visible_nan_beside_a_page_that_is_none(Dh, fmt, what):
         else:
             want[:] = True
         assert torch.equal(~ok, want)
+
+
+# ------------------------------------------------------------------------- V scales that are far apart ----
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("Dh", [64, 128, 256])
+@pytest.mark.parametrize("up", [12, 22, 34, 90])
+def test_hidden_scales_do_not_reach_a_row(Dh, fmt, up):
+    """A later token, or one behind the window, whose V scale is 2^up times the others'."""
+    n, new, bs = 150, 100, 16
+    for j, window, sinks in ((140, 0, 0), (141, 60, 3), (20, 40, 2)):
+        k, v, table, ln = make_caches([n], 1, Dh, bs, fmt, seed=211)
+        blk, at = slot(table, 0, j, bs)
+        v.scale_inv[blk, at] *= 2.0 ** up
+        q = inputs.normal_bf16((new, 2, Dh), 1.0, seed=212).to(DEV)
+        out, lse = prefill(q, [0, new], k, v, table, ln, window, sinks)
+        rows = [(t, 0, n - new + t) for t in (0, 1, 8, 9, 10, 11, 50, 77, 89, 90, 91, 99)]
+        bounds.check(out, lse, q, k, v, table, [n], rows, Dh ** -0.5, window, sinks)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("Dh,H,G,lens", [(128, 2, 3, [300]), (64, 4, 1, [150] * 60), (256, 1, 5, [200, 33]),
+                                         (128, 1, 1, [3000])])
+@pytest.mark.parametrize("bits", [10, 16, 40])
+def test_prefill_scales_spread_at_random(Dh, H, G, lens, fmt, bits):
+    """Scales over a range of 2^bits: units that one block covers and units that several do."""
+    bs, new = 24, 40
+    k, v, table, ln = make_caches(lens, H, Dh, bs, fmt, seed=221)
+    g = torch.Generator().manual_seed(222)
+    v.scale_inv.mul_(2.0 ** (bits * torch.rand(v.scale_inv.shape, generator=g)).floor().to(DEV))
+    news = [min(n, new) for n in lens]
+    off = torch.tensor([0] + news).cumsum(0)
+    q = inputs.normal_bf16((int(off[-1]), H * G, Dh), 1.0, seed=223).to(DEV)
+    out, lse = prefill(q, off, k, v, table, ln)
+    some = range(len(lens)) if len(lens) < 5 else (0, 1, 30, len(lens) - 1)
+    rows = [(int(off[b]) + i, b, lens[b] - news[b] + i) for b in some for i in (0, 17, news[b] - 1)]
+    bounds.check(out, lse, q, k, v, table, lens, rows, Dh ** -0.5)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -12])
+def test_padding_tokens_of_zeros(fmt, size):
+    """V rows of zeros, whose scale is 1 whatever the others' are."""
+    n, new, bs, Dh = 400, 30, 16, 128
+    k, v, table, ln = make_caches([n], 2, Dh, bs, fmt, seed=231)
+    x = inputs.normal_bf16((n, 2, Dh), size, seed=232)
+    zero = torch.rand(n, generator=torch.Generator().manual_seed(233)) < 0.2
+    zero[: 130] = False
+    x[zero] = 0
+    _, slots = inputs.paged_layout([n], bs, k.num_blocks, 231)
+    v.write(x.to(DEV), slots.to(DEV))
+    q = inputs.normal_bf16((new, 4, Dh), 1.0, seed=234).to(DEV)
+    out, lse = prefill(q, [0, new], k, v, table, ln)
+    rows = [(t, 0, n - new + t) for t in (0, 13, 29)]
+    bounds.check(out, lse, q, k, v, table, [n], rows, Dh ** -0.5)
+    one, l1 = fp8q.paged_attention_decode(q[-1:], k, v, table, ln)
+    bounds.check(one, l1, q[-1:], k, v, table, [n], [(0, 0, n - 1)], Dh ** -0.5, prefill=False)
+
+
+def steered(n, Dh, H, G, new, bs, fmt, seed, logits):
+    """Caches whose token j has a logit near logits[j] (natural units, softmax scale 1) for every query."""
+    k, v, table, ln = make_caches([n], H, Dh, bs, fmt, seed=seed)
+    _, slots = inputs.paged_layout([n], bs, k.num_blocks, seed)
+    u = torch.ones(Dh) / Dh ** 0.5
+    k.write((logits[:, None, None] * u + inputs.normal_bf16((n, H, Dh), 0.05, seed=seed + 1).float()).bfloat16().to(DEV),
+            slots.to(DEV))
+    q = (u + inputs.normal_bf16((new, H * G, Dh), 0.02, seed=seed + 2).float()).bfloat16().to(DEV)
+    return k, v, table, ln, q
+
+
+def both(k, v, table, ln, q, n, scale=1.0, copies=1):
+    """Prefill of q for as many sequences over the same pages: one is split over many
+    thread blocks, of many each block takes whole ones."""
+    new = q.shape[0]
+    many, lens, off = table.repeat(copies, 1), ln.repeat(copies), torch.arange(copies + 1) * new
+    out, lse = prefill(q.repeat(copies, 1, 1), off, k, v, many, lens, softmax_scale=scale)
+    some = sorted({0, copies // 3, copies - 1})
+    rows = [(c * new + t, c, n - new + t) for c in some for t in (0, new // 2, new - 1)]
+    bounds.check(out, lse, q.repeat(copies, 1, 1), k, v, many, [n] * copies, rows, scale)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("Dh", [64, 128, 256])
+@pytest.mark.parametrize("j,copies", [(0, 1), (100, 1), (630, 1), (0, 160), (630, 160)])
+def test_a_large_value_that_hardly_counts(Dh, fmt, j, copies):
+    """A visible token with a V scale 2^40 times the others' and a weight of e^-60 or so."""
+    n, bs = 700, 16
+    logits = torch.zeros(n)
+    logits[j] = -60.0
+    k, v, table, ln, q = steered(n, Dh, 1, 3, 40, bs, fmt, 241, logits)
+    blk, at = slot(table, 0, j, bs)
+    v.scale_inv[blk, at] *= 2.0 ** 40
+    both(k, v, table, ln, q, n, copies=copies)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("Dh", [64, 128, 256])
+@pytest.mark.parametrize("n,slope", [(400, 0.25), (400, -0.25), (400, 0.05), (3000, 0.02), (3000, -0.02)])
+@pytest.mark.parametrize("copies", [1, 160])
+def test_weights_and_scales_that_cancel(Dh, fmt, n, slope, copies):
+    """Logits that rise or fall by up to 100 along the sequence, in steps of a few per tile or fractions of one, while
+    the V scales go the other way: every token counts."""
+    bs = 16
+    logits = slope * (torch.arange(n, dtype=torch.float32) - n / 2)
+    k, v, table, ln, q = steered(n, Dh, 1, 2, 40, bs, fmt, 251, logits)
+    at = inputs.paged_layout([n], bs, k.num_blocks, 251)[1].to(DEV)
+    v.scale_inv.view(-1)[at] *= (2.0 ** (-logits / math.log(2)).round()).to(DEV)
+    both(k, v, table, ln, q, n, copies=copies)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("e", [127, 126, 120, -110])
+def test_scales_at_the_ends_of_their_type(fmt, e):
+    """Every V scale 2^e, with codes so small that the values and their sums are finite."""
+    n, bs, Dh = (60, 16, 64) if e > 0 else (300, 16, 64)
+    k, v, table, ln = make_caches([n], 1, Dh, bs, fmt, seed=261)
+    g = torch.Generator().manual_seed(262)
+    lo, hi = (1, 8) if e > 0 else (0x10, 0x30)
+    codes = torch.randint(lo, hi, v.cache.shape, generator=g, dtype=torch.uint8)
+    codes |= torch.randint(0, 2, v.cache.shape, generator=g, dtype=torch.uint8) << 7
+    v.cache.copy_(codes)
+    v.scale_inv.fill_(2.0 ** e)
+    q = inputs.normal_bf16((20, 2, Dh), 1.0, seed=263).to(DEV)
+    both(k, v, table, ln, q, n, Dh ** -0.5)
