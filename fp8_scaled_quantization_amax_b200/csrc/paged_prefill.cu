@@ -528,6 +528,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     __shared__ uint32_t s_tmem, s_abort, s_poison, s_qmax[MT][4];
     __shared__ uint32_t s_progress;   // tiles whose weights all softmax warps have handed over
     __shared__ float4 s_factor[MT][2][KT / 4];   // column factors of a row tile's softmax, two tiles
+    __shared__ float s_ones[KT];      // in their place where the products have been multiplied by them
     volatile uint32_t *abort_flag = &s_abort;
     const uint32_t sb = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
@@ -563,6 +564,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         s_abort = s_poison = s_progress = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (threadIdx.x < KT) s_ones[threadIdx.x] = 1.0f;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                      "r"(TMEM_COLS)
@@ -942,7 +944,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             int eo = kNoScale;                // O is in units of 2^eo
             for (int k = 0; k < len; ++k, ++kc, ++sc) {
                 const uint32_t m = sb + P::OFF_M + (kc % P::META) * P::M_BYTES;
-                const uint32_t fk = smem_u32(s_factor[mi][kc & 1]);
+                uint32_t fk = smem_u32(s_factor[mi][kc & 1]);
                 const int j0 = tile_pos<KT>(u, tile + k);
                 // The columns' factors, before S is ready where their look-up can be waited for: from the second
                 // tile of a run on, when the one before it in the ring is known to be past (a parity only tells a
@@ -1008,6 +1010,12 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                         if (bad && top > kNoMax) {
                             dm = mr - (top - kBelow);
                             mr = top - kBelow;
+                        }
+                        if (__any_sync(0xFFFFFFFFu, raise && top > kNoMax && fabsf(top) >= 0x1p24f)) {
+                            // The sweep subtracts the reference from the exact product, which can lie above the
+                            // rounded one by 2^-24 of it.  Where that counts, the rounded products go into S.
+                            scale_s([&](int c) { return __uint_as_float(ld_shared_u32(fk + 4 * c)); });
+                            fk = smem_u32(s_ones);
                         }
                         again |= raise;
                         hide = false;

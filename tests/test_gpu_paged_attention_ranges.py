@@ -7,6 +7,7 @@ import torch
 
 from fp8_scaled_quantization_amax_b200 import fp8q, inputs
 from tests import paged_bounds as bounds
+from tests import paged_ref as ref
 from tests.test_gpu_paged_attention import DEV, make_caches
 
 pytestmark = pytest.mark.gpu
@@ -171,3 +172,32 @@ def test_scales_at_the_ends_of_their_type(fmt, e):
     v.scale_inv.fill_(2.0 ** e)
     q = inputs.normal_bf16((20, 2, Dh), 1.0, seed=263).to(DEV)
     both(k, v, table, ln, q, n, Dh ** -0.5)
+
+
+# ------------------------------------------------------------------------------ logits out of the ordinary ----
+
+@pytest.mark.parametrize("big", [1.0, 2.0 ** 20, 2.0 ** 24, 2.0 ** 33, 1e20, -1e20, 1e30])
+@pytest.mark.parametrize("Dh", [64, 128, 256])
+def test_logits_past_two_to_the_31(Dh, big):
+    """Logits up to 8 |big| Dh, no two tokens' closer than 2^-9 of that: nothing but the largest visible one counts."""
+    n, new, bs = 300, 140, 16
+    k, v, table, ln = make_caches([n], 1, Dh, bs, 0, seed=281)
+    _, slots = inputs.paged_layout([n], bs, k.num_blocks, 281)
+    level = torch.linspace(-8, 8, n)[torch.randperm(n, generator=torch.Generator().manual_seed(282))]
+    k.cache.view(-1, 1, Dh)[slots.to(DEV)] = 0x7E                      # 448
+    k.scale_inv.view(-1, 1)[slots.to(DEV)] = (level / 448)[:, None].to(DEV)
+    q = torch.full((new, 3, Dh), big, dtype=torch.bfloat16, device=DEV)
+    scale = 32768.0 if abs(big) == 1.0 else 1.0                       # 8 Dh 2^15 is past 2^24 too
+    host = ref.Cache(k, v)
+    th, visible = table.cpu()[0].tolist(), torch.arange(n)
+    for window, sinks in ((0, 0), (50, 2)):
+        out, lse = prefill(q, [0, new], k, v, table, ln, window, sinks, softmax_scale=scale)
+        one, l1 = fp8q.paged_attention_decode(q[-1:], k, v, table, ln, window, sinks, softmax_scale=scale)
+        z = level.double() * float(q[0, 0, 0]) * Dh * scale
+        for got, gl, p in [(out[t], lse[t], n - new + t) for t in (0, 1, 40, 100, new - 1)] + [(one[0], l1[0], n - 1)]:
+            sees = (visible <= p) & ((window == 0) | (visible > p - window) | (visible < sinks))
+            j = int(torch.where(sees, z, -math.inf).argmax())
+            want = host.v[ref.slot_of(th, j, bs, k.num_blocks), 0]
+            # V times its scale in fp16 (two roundings of 2^-11, weights and result one of 2^-11 and 2^-8)
+            assert torch.all((got.float().cpu().double() - want).abs() <= (2.0 ** -8 + 2.0 ** -9) * want.abs()), (p, j)
+            assert torch.all((gl.cpu().double() - z[j]).abs() <= Dh * 2.0 ** -23 * abs(float(z[j]))), (p, j)
