@@ -525,7 +525,8 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // s_poison: something was taken out of V (for good: later results of this CTA look again for nothing)
-    __shared__ uint32_t s_tmem, s_abort, s_poison, s_qmax[MT][4];
+    __shared__ uint32_t s_tmem, s_abort, s_poison;
+    __shared__ uint2 s_q[MT][4];      // largest and smallest row exponent of Q, per softmax warp
     __shared__ uint32_t s_progress;   // tiles whose weights all softmax warps have handed over
     __shared__ float4 s_factor[MT][2][KT / 4];   // column factors of a row tile's softmax, two tiles
     __shared__ float s_ones[KT];      // in their place where the products have been multiplied by them
@@ -848,7 +849,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"(2 + mi), "r"((uint32_t)x) : "memory");
             return r != 0;
         };
-        // S times f(column); rare, so eight columns of code
+        // S times f(column), first x, then y; rare, so eight columns of code
         auto scale_s = [&](auto f) {
 #pragma unroll 1
             for (int c = 0; c < KT; c += 8) {
@@ -856,7 +857,10 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 tmem_ld8_async(ts + c, x);
                 tmem_ld_wait(x);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f(c + i));
+                for (int i = 0; i < 8; ++i) {
+                    const float2 by = f(c + i);
+                    x[i] = __float_as_uint(__uint_as_float(x[i]) * by.x * by.y);
+                }
                 tmem_st4(ts + c, x[0], x[1], x[2], x[3]);
                 tmem_st4(ts + c + 4, x[4], x[5], x[6], x[7]);
             }
@@ -864,7 +868,8 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         };
         uint32_t kc = 0, sc = 0;              // tiles of the CTA; S tiles of this row tile
         // the rows of this row tile in the run; Q as fp16
-        int p = -1, wb = 0;
+        int p = -1, wb = 0, qs = 0;           // qs: exponent of the row's Q less the tile's, where the warp's are `apart`
+        bool apart = false;
         int64_t orow = 0;
         bool valid = false;
         float qf = 0.0f;
@@ -882,10 +887,11 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             p = valid ? u.n - u.count + tok : -1;
             wb = p >= 0 ? pv.window_begin(p) : 0;
             orow = (u.t0 + tok) * (int64_t)pv.H * a.G + (int64_t)run.h * a.G + g;
-            // A warp copies its 32 rows as they are, whole rows at a time, then scales them in place, each thread what
-            // it copied; short loops, since code that runs once per unit comes from far away.  One power of two for
-            // the tile's 128 rows (an element loses something only below 2^-29 of the tile's largest, and then 2^-40
-            // of that in the logits).
+            // A warp copies its 32 rows as they are, whole rows at a time; then each thread scales its own row in place,
+            // in short loops, since code that runs once per unit comes from far away.  One power of two for the tile's
+            // 128 rows: an element loses something only below 2^-31 of the tile's largest, so a row 2^-15 of it keeps
+            // all down to 2^-16 of its own largest, and what it loses below stays under 2^-24 of that.  Rows further
+            // apart than 2^15 get a power of two each, which S is then multiplied back by.
             constexpr int QC = DH / 8, QR = 32 / QC, QN = 32 / QR;    // 16-byte chunks of a row; rows per copy; copies
             const int qc = lane % QC, r0 = (warp & 3) * 32 + lane / QC;
             auto at_row = [&](int i) -> uint32_t {
@@ -904,31 +910,37 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                              : "memory");
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
-            auto own = [&](int i) -> uint4 {
-                const float4 w = ld_shared_f4(at_row(i));
+            __syncwarp();
+            auto own = [&](int i) -> uint32_t { return sb + mi * P::QB + (i >> 3) * (128 * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4); };
+            auto ld = [&](int i) -> uint4 {
+                const float4 w = ld_shared_f4(own(i));
                 return make_uint4(__float_as_uint(w.x), __float_as_uint(w.y), __float_as_uint(w.z), __float_as_uint(w.w));
             };
             uint32_t mx = 0;
 #pragma unroll 4
-            for (int i = 0; i < QN; ++i) mx = amax_fast8(mx, own(i));
+            for (int i = 0; i < QC; ++i) mx = amax_fast8(mx, ld(i));
             mx = amax_fast_final(mx);
             if (mx == 0xFFFFFFFFu) {          // a NaN or infinity: the finite elements' maximum
                 mx = 0;
                 uint32_t bad = 0;
 #pragma unroll 1
-                for (int i = 0; i < QN; ++i) mx = amax_exact8(mx, own(i), bad);
+                for (int i = 0; i < QC; ++i) mx = amax_exact8(mx, ld(i), bad);
             }
-            mx = __reduce_max_sync(0xFFFFFFFFu, mx);
-            if (lane == 0) s_qmax[mi][warp & 3] = mx;
+            const uint32_t er = max(mx >> 7, 14u);               // exponent + 127; a row of zeros takes any
+            const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, er), lo = __reduce_min_sync(0xFFFFFFFFu, mx ? er : 255u);
+            if (lane == 0) s_q[mi][warp & 3] = make_uint2(hi, lo);
             wg_sync();
-            mx = max(max(s_qmax[mi][0], s_qmax[mi][1]), max(s_qmax[mi][2], s_qmax[mi][3]));
-            const int e = max((int)(mx >> 7), 14) - 127;
-            const float up = a.scale < 0.0f ? -pow2i(14 - e) : pow2i(14 - e);   // the sign of the scale goes to Q
+            const uint2 e0 = s_q[mi][0], e1 = s_q[mi][1], e2 = s_q[mi][2], e3 = s_q[mi][3];
+            const int top = (int)max(max(e0.x, e1.x), max(e2.x, e3.x)), least = (int)min(min(e0.y, e1.y), min(e2.y, e3.y));
+            apart = least < top - 15;
+            qs = apart && mx ? (int)er - top : 0;
+            const int e = top - 127;
+            const float up = a.scale < 0.0f ? -pow2i(14 - e - qs) : pow2i(14 - e - qs);   // the sign of the scale goes to Q
             qf = pow2i(e) * 0x1p-14f;
 #pragma unroll 2
-            for (int i = 0; i < QN; ++i) {
-                const uint4 v = own(i);
-                st_shared16(at_row(i), pack_f16x2(bf_lo(v.x) * up, bf_hi(v.x) * up),
+            for (int i = 0; i < QC; ++i) {
+                const uint4 v = ld(i);
+                st_shared16(own(i), pack_f16x2(bf_lo(v.x) * up, bf_hi(v.x) * up),
                             pack_f16x2(bf_lo(v.y) * up, bf_hi(v.y) * up), pack_f16x2(bf_lo(v.z) * up, bf_hi(v.z) * up),
                             pack_f16x2(bf_lo(v.w) * up, bf_hi(v.w) * up));
             }
@@ -973,11 +985,15 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                 uint32_t pk[KT / 2];
                 float dm = 0.0f, sum = 0.0f;  // the old reference less the new one
                 bool again = k == 0, bad = again, hide = masked;
-                if (odd_column)
+                if (odd_column || apart) {
+                    // S by the rows' own powers of two, in two steps (2^qs may be less than a float), and by the
+                    // columns' odd factors
+                    const float q0 = pow2i(qs >> 1), q1 = pow2i(qs - (qs >> 1));
                     scale_s([&](int c) {
                         const float o = __uint_as_float(ld_shared_u32(m + P::M_DK + 4 * c)) * qf;
-                        return o > 0.0f && o < INFINITY ? 1.0f : o;
+                        return o > 0.0f && o < INFINITY ? make_float2(q0, q1) : make_float2(q0 * q1, o);
                     });
+                }
                 while (true) {
                     const bool raise = __any_sync(0xFFFFFFFFu, bad);
                     if (hide || raise) {
@@ -1014,7 +1030,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                         if (__any_sync(0xFFFFFFFFu, raise && top > kNoMax && fabsf(top) >= 0x1p24f)) {
                             // The sweep subtracts the reference from the exact product, which can lie above the
                             // rounded one by 2^-24 of it.  Where that counts, the rounded products go into S.
-                            scale_s([&](int c) { return __uint_as_float(ld_shared_u32(fk + 4 * c)); });
+                            scale_s([&](int c) { return make_float2(__uint_as_float(ld_shared_u32(fk + 4 * c)), 1.0f); });
                             fk = smem_u32(s_ones);
                         }
                         again |= raise;

@@ -201,3 +201,22 @@ def test_logits_past_two_to_the_31(Dh, big):
             # V times its scale in fp16 (two roundings of 2^-11, weights and result one of 2^-11 and 2^-8)
             assert torch.all((got.float().cpu().double() - want).abs() <= (2.0 ** -8 + 2.0 ** -9) * want.abs()), (p, j)
             assert torch.all((gl.cpu().double() - z[j]).abs() <= Dh * 2.0 ** -23 * abs(float(z[j]))), (p, j)
+
+
+# --------------------------------------------------------------------- queries that are far apart ----
+
+@pytest.mark.parametrize("big", [1e20, 2.0 ** 100, 2.0 ** 14, 2.0 ** -60])
+@pytest.mark.parametrize("Dh", [64, 128, 256])
+def test_a_finite_query_row_leaves_the_others_their_bits(Dh, big):
+    """One row 2^14 to 2^100 times the others in the same tile (or far below them), in the first or the second tile."""
+    n, new, bs, G = 300, 100, 16, 4
+    k, v, table, ln = make_caches([n], 2, Dh, bs, 0, seed=271)
+    q = inputs.normal_bf16((new, 2 * G, Dh), 1.0, seed=272)
+    for t in (17, 80):
+        q[t, 1] = (q[t, 1].float() * big).bfloat16()
+    q = q.to(DEV)
+    for scale in (Dh ** -0.5, -0.1):
+        out, lse = prefill(q, [0, new], k, v, table, ln, 150, 2, softmax_scale=scale)
+        rows = [(t, 0, n - new + t) for t in (0, 16, 17, 18, 31, 63, 64, 80, 81, 99)]
+        s = float(torch.tensor(scale))
+        bounds.check(out, lse, q, k, v, table, [n], rows, s, 150, 2)
