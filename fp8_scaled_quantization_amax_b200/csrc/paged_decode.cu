@@ -22,7 +22,8 @@
 //   * Q's rows are brought to [2^14, 2^15) by a power of two before they become
 //     fp16, which is then exact for every element above 2^-24 of the row's
 //     largest; the weights times V's scales are normalised by a running power
-//     of two, so that fp16 holds them to 2^-11 down to 2^-22 of the largest;
+//     of two of each query head, so that fp16 holds them to 2^-11 down to 2^-19
+//     of the largest product (a large scale that hardly weighs does not count);
 //   * the maximum is only moved when a logit passes it by 2^6 (one vote per
 //     tile instead of shuffles); weights stay below 2^6, far inside fp16.
 //
@@ -52,6 +53,7 @@ constexpr int kTile = 32;                    // positions per warp and step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.0e38f;           // before the first logit; below every finite logit that matters
 constexpr float kLazy = 6.0f;                // log2 of how far a logit may pass the maximum in use
+constexpr int kMaxUnit = 120;                // log2 of the largest power of two on the weights: 2^kLazy of them are finite
 
 struct DecodeArgs {
     const __nv_bfloat16 *q;
@@ -296,7 +298,7 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
         const int tile_end = (int)min((int64_t)nt, tile + (end - at));
         const int vh = row * a.HB + hw, h = vh / a.GC, chunk = vh % a.GC;
 
-        float o[NT][MI][4], m[NT][2], l[NT][2], vscale = 1.0f, vcap = 0.0f;
+        float o[NT][MI][4], m[NT][2], l[NT][2], vs[NT][2];   // O^T is held times the power of two vs
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
 #pragma unroll
@@ -305,6 +307,7 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
                 for (int e = 0; e < 4; ++e) o[x][i][e] = 0.0f;
             m[x][0] = m[x][1] = kNoMax;
             l[x][0] = l[x][1] = 0.0f;
+            vs[x][0] = vs[x][1] = pow2i(kMaxUnit);
         }
 
         const uint8_t *kh = pv.kc + (int64_t)h * pv.Dh + 16 * t, *vhp = pv.vc + (int64_t)h * pv.Dh + 16 * t;
@@ -503,9 +506,15 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
                         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
                         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
-                        const float al = exp2_fast(m[x][e] - v);
+                        // what O^T holds shrinks by 2^dm: its power of two grows by as many whole steps as the
+                        // maximum passes, which come to within one of it however often it moves
+                        const float dm = m[x][e] - v;
+                        const int was = (int)(__float_as_uint(vs[x][e]) >> 23) - 127;
+                        const int now = min(kMaxUnit, was + (int)fminf(floorf(v) - floorf(m[x][e]), 1000.0f));
                         m[x][e] = v;
-                        l[x][e] *= al;
+                        l[x][e] *= exp2_fast(dm);
+                        vs[x][e] = pow2i(now);
+                        const float al = exp2_fast(dm + (float)(now - was));
 #pragma unroll
                         for (int i = 0; i < MI; ++i) {
                             o[x][i][e] *= al;
@@ -530,34 +539,50 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
             un = data + (uint32_t)(read * C::UNIT);
             ax = aux + (uint32_t)(read * C::AUX);
             if constexpr (TMA) wait_bar(bars + 8 * read, phase, &s_abort, kErrProducer);
-            // ---- the power of two that V's scales are held against
+            // ---- weights times V's scales, under the power of two that keeps them in fp16
             float dv[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) dv[y] = lds_f(ax + 4 * (8 * y + g));
             const float dmax = fmaxf(fmaxf(fabsf(dv[0]), fabsf(dv[1])), fmaxf(fabsf(dv[2]), fabsf(dv[3])));
-            if (__any_sync(0xFFFFFFFFu, dmax > vcap && dmax < INFINITY)) {
-                const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, dmax < INFINITY ? __float_as_uint(dmax) : 0u);
-                const int ex = max((int)(bits >> 23) - 127, -100);             // dmax < 2^(ex + 1)
-                const float vs = pow2i(8 - ex), r = vcap > 0.0f ? vs / vscale : 1.0f;
-                vscale = vs;                                                   // dv * vscale < 2^9
-                vcap = pow2i(ex + 1);
+            float vmax = vs[0][0];
+#pragma unroll
+            for (int x = 0; x < NT; ++x) vmax = fmaxf(vmax, fmaxf(vs[x][0], vs[x][1]));
+            if (__any_sync(0xFFFFFFFFu, dmax * vmax >= 512.0f && dmax < INFINITY)) {   // else below 2^9 2^kLazy = 2^15
+                // the largest product of each query head, to [2^6, 2^7) where it is more: scales up to four times
+                // as large do not come here again
 #pragma unroll
                 for (int x = 0; x < NT; ++x)
 #pragma unroll
-                    for (int i = 0; i < MI; ++i)
+                    for (int e = 0; e < 2; ++e) {
+                        float top = 0.0f;             // times 2^-16, which keeps it finite
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[x][i][e] *= r;
+                        for (int y = 0; y < 4; ++y) {
+                            const float w = fabsf(s[y / 2][x][2 * (y & 1) + e] * (dv[y] * 0x1p-16f));
+                            top = fmaxf(top, w < INFINITY ? w : 0.0f);
+                        }
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+                        const int was = (int)(__float_as_uint(vs[x][e]) >> 23) - 127;
+                        const int now = min(was, -10 - ((int)(__float_as_uint(top) >> 23) - 127));
+                        const float r = exp2_fast((float)(now - was));
+                        vs[x][e] = pow2i(now);
+#pragma unroll
+                        for (int i = 0; i < MI; ++i) {
+                            o[x][i][e] *= r;
+                            o[x][i][2 + e] *= r;
+                        }
+                    }
             }
             uint32_t pb[2][NT][2];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const float f0 = dv[2 * y] * vscale, f1 = dv[2 * y + 1] * vscale;
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-                for (int x = 0; x < NT; ++x) {
-                    pb[y][x][0] = transpose8x8(pack_f16x2(s[y][x][0] * f0, s[y][x][1] * f0));
-                    pb[y][x][1] = transpose8x8(pack_f16x2(s[y][x][2] * f1, s[y][x][3] * f1));
-                }
-            }
+                for (int x = 0; x < NT; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        pb[y][x][e] = transpose8x8(pack_f16x2(s[y][x][2 * e] * vs[x][0] * dv[2 * y + e],
+                                                              s[y][x][2 * e + 1] * vs[x][1] * dv[2 * y + e]));
             // ---- O^T += V^T P^T.  A weight of zero does not hide what a slot that is not visible holds (it
             // may be a NaN code): such rows of a box become zeros, each by the lane that reads it next.
             if (TMA && seen != 0xFFFFFFFFu) {
@@ -616,11 +641,12 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
         // ---- this run of tiles is done: result, or a part of one
         // o[..][i] holds the head elements dh_of(i) and the next one
         auto dh_of = [&](int i) { return VB == 8 ? 8 * g + 2 * i : 128 * (i >> 3) + 16 * g + 2 * (i & 7); };
-        const float inv = 1.0f / vscale;
+        float inv[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                inv[x][e] = 1.0f / vs[x][e];
                 float v = l[x][e];
                 v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
                 v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
@@ -645,7 +671,7 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
                     const int col = 8 * x + 2 * t + e, gi = chunk * C::COLS + col;
                     if (gi >= a.G) continue;
                     if (whole) {
-                        const float r = l[x][e] == 0.0f ? 0.0f : inv / l[x][e];
+                        const float r = l[x][e] == 0.0f ? 0.0f : inv[x][e] / l[x][e];
                         const int64_t orow = (int64_t)b * pv.H * a.G + h * a.G + gi;
                         if (g == 0) a.lse[orow] = l[x][e] == 0.0f ? -INFINITY : (m[x][e] + log2f(l[x][e])) * kLn2;
                         __nv_bfloat16 *op = a.out + orow * pv.Dh;
@@ -666,8 +692,8 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
 #pragma unroll
                         for (int i = 0; i < MI; i += 2)
                             *reinterpret_cast<float4 *>(pp + dh_of(i)) =
-                                make_float4(o[x][i][e] * inv, o[x][i][2 + e] * inv, o[x][i + 1][e] * inv,
-                                            o[x][i + 1][2 + e] * inv);
+                                make_float4(o[x][i][e] * inv[x][e], o[x][i][2 + e] * inv[x][e],
+                                            o[x][i + 1][e] * inv[x][e], o[x][i + 1][2 + e] * inv[x][e]);
                     }
                 }
         } else {
@@ -685,7 +711,7 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
 #pragma unroll
                     for (int i = 0; i < MI; ++i)
                         *reinterpret_cast<float2 *>(mine + col * DH + dh_of(i)) =
-                            make_float2(o[x][i][e] * inv, o[x][i][2 + e] * inv);
+                            make_float2(o[x][i][e] * inv[x][e], o[x][i][2 + e] * inv[x][e]);
                 }
             __syncthreads();
             // four elements per thread and step

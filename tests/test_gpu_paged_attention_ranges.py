@@ -119,7 +119,7 @@ def steered(n, Dh, H, G, new, bs, fmt, seed, logits):
 
 
 def both(k, v, table, ln, q, n, scale=1.0, copies=1):
-    """Prefill of q for as many sequences over the same pages: one is split over many
+    """Prefill of q and decode of its last row, for as many sequences over the same pages: one is split over many
     thread blocks, of many each block takes whole ones."""
     new = q.shape[0]
     many, lens, off = table.repeat(copies, 1), ln.repeat(copies), torch.arange(copies + 1) * new
@@ -127,6 +127,9 @@ def both(k, v, table, ln, q, n, scale=1.0, copies=1):
     some = sorted({0, copies // 3, copies - 1})
     rows = [(c * new + t, c, n - new + t) for c in some for t in (0, new // 2, new - 1)]
     bounds.check(out, lse, q.repeat(copies, 1, 1), k, v, many, [n] * copies, rows, scale)
+    last = q[-1:].repeat(copies, 1, 1)
+    one, l1 = fp8q.paged_attention_decode(last, k, v, many, lens, softmax_scale=scale)
+    bounds.check(one, l1, last, k, v, many, [n] * copies, [(c, c, n - 1) for c in some], scale, prefill=False)
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
