@@ -293,6 +293,7 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
     auto k_chunk = [](int t, int c) { return DH == 64 ? t : (c >> 1) * 8 + 2 * t + (c & 1); };
     int fill = 0, read = 0;                   // units of the ring to copy into and to read
     uint32_t phase = 0;                       // parity of the unit to read
+    bool dead = false;                        // a wait of this warp ran out: nothing more is copied or computed
 
     while (true) {
         const int tile_end = (int)min((int64_t)nt, tile + (end - at));
@@ -330,11 +331,10 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
         };
         // K or V of that tile into the next unit
         auto issue = [&](const CUtensorMap *map, const uint8_t *codes, const float *scales, bool is_k) {
-            if (fetch < tile_end) {           // the same for all lanes
+            if (fetch < tile_end && !dead) {  // the same for all lanes
                 const uint32_t mask = __ballot_sync(0xFFFFFFFFu, live);
                 const uint32_t dst = data + (uint32_t)(fill * C::UNIT), ax = aux + (uint32_t)(fill * C::AUX);
                 if constexpr (TMA) {
-                  if (!*reinterpret_cast<volatile uint32_t *>(&s_abort)) {   // after a wait that ran out: no more copies
                     const uint32_t bar = bars + 8 * fill;
                     if (lane == 0) mbar_expect_tx(bar, C::UNIT);
                     if ((lane & (a.box - 1)) == 0) {
@@ -344,7 +344,6 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
                         tma_load_3d(dst + (uint32_t)(lane * (DH == 64 ? 64 : 128)), map, bar, 0, h, z);
                         if (DH == 256) tma_load_3d(dst + 4096u + (uint32_t)(lane * 128), map, bar, 128, h, z);
                     }
-                  }
                 } else {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
@@ -376,6 +375,25 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
                 read = 0;
                 phase ^= 1u;
             }
+        };
+        // The copies of the unit to read have landed.  Where that wait runs out the warp waits (again with a limit) for
+        // every copy it has in flight, so that none lands in memory that has another use by then.
+        auto landed = [&]() -> bool {
+            if constexpr (TMA) {
+                if (__all_sync(0xFFFFFFFFu, wait_bar(bars + 8 * read, phase, &s_abort, kErrProducer))) return true;
+                dead = true;
+                uint32_t at_phase = phase;
+                for (int u = read, left = fill > read ? fill - read : fill - read + C::UNITS; left > 0; --left) {
+                    wait_bar_drain(bars + 8 * u, at_phase);
+                    if (++u == C::UNITS) {
+                        u = 0;
+                        at_phase ^= 1u;
+                    }
+                }
+                __syncwarp();
+                return false;
+            }
+            return true;
         };
         look_up();
         // the ring's last unit is filled when the one that was read before it is done with
@@ -423,12 +441,12 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
             cf[x][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
         }
 
-        for (int k = 0; k < ntile; ++k) {
+        for (int k = 0; k < ntile && !dead; ++k) {
             asm volatile("cp.async.wait_group %0;" ::"n"(C::UNITS - 2) : "memory");
             __syncwarp();                     // the other lanes' copies; and the unit read before is done with
             if constexpr (C::UNITS % 2) issue_k(); else issue_v();
             uint32_t un = data + (uint32_t)(read * C::UNIT), ax = aux + (uint32_t)(read * C::AUX), seen;
-            if constexpr (TMA) wait_bar(bars + 8 * read, phase, &s_abort, kErrProducer);
+            if (!landed()) break;
             asm volatile("ld.shared.u32 %0, [%1];" : "=r"(seen) : "r"(ax + 128));
 
             // ---- S^T = K Q^T, 16 positions at a time
@@ -538,7 +556,7 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
             if constexpr (C::UNITS % 2) issue_v(); else issue_k();
             un = data + (uint32_t)(read * C::UNIT);
             ax = aux + (uint32_t)(read * C::AUX);
-            if constexpr (TMA) wait_bar(bars + 8 * read, phase, &s_abort, kErrProducer);
+            if (!landed()) break;
             // ---- weights times V's scales, under the power of two that keeps them in fp16
             float dv[4];
 #pragma unroll
