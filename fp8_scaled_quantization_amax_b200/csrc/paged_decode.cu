@@ -900,6 +900,7 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 // A CTA's warps share out the largest power of two of heads that divides their
 // number, so that no warp is idle; the warps left per head take turns at its
 // tiles.
+// max_context: positions of a sequence that the call may look at.
 DecodePlan decode_plan(int64_t B, int64_t Hq, int64_t H, int64_t Dh, int64_t max_context, bool weights, int sms) {
     DecodePlan p;
     p.G = (int)(Hq / H);
@@ -1009,11 +1010,13 @@ extern "C" fp8_status fp8_paged_attention_decode(
     int sms;
     st = check_device(&sms);
     if (st != FP8_OK) return st;
-    const int64_t context = max_blocks * block_size;
-    const DecodePlan p = decode_plan(B, Hq, H, Dh, context, mass != nullptr, sms);
-    if (!workspace || workspace_bytes < p.total()) return FP8_ERR_INVALID_ARG;
     const PagedView pv = make_paged_view(k_cache, k_scale, v_cache, v_scale, H, Dh, block_size, num_blocks,
                                          block_table, seq_lens, max_blocks, window, sinks);
+    int64_t context = max_blocks * block_size;
+    // whole tiles: at most one begun for the sinks and two for the window
+    if (pv.window > 0) context = std::min<int64_t>(context, (int64_t)pv.window + pv.sinks + 3 * kTile);
+    const DecodePlan p = decode_plan(B, Hq, H, Dh, context, mass != nullptr, sms);
+    if (!workspace || workspace_bytes < p.total()) return FP8_ERR_INVALID_ARG;
     uint8_t *ws = (uint8_t *)workspace;
     DecodeArgs a = {};
     a.q = (const __nv_bfloat16 *)q_bf16;
@@ -1030,9 +1033,7 @@ extern "C" fp8_status fp8_paged_attention_decode(
     a.lse = lse ? lse : (float *)(ws + p.part_bytes + p.span_bytes);
     if (mass && ld_mass > 0 && context > 0) {
         a.logits = (float *)(ws + p.part_bytes + p.span_bytes + p.lse_bytes);
-        // whole tiles: at most one begun for the sinks and two for the window
         a.vis_max = (context + kTile - 1) / kTile * kTile;
-        if (pv.window > 0) a.vis_max = std::min<int64_t>(a.vis_max, (int64_t)pv.window + pv.sinks + 3 * kTile);
         a.mass = mass;
         a.ld_mass = ld_mass;
         a.decay = mass_decay;

@@ -632,8 +632,9 @@ def _table_shape(block_table, seq_lens, what="block_table"):
 
 
 def paged_attention_workspace(B, Hq, H, Dh, max_context=0, weights=False, tokens=0, device="cuda"):
-    """Scratch of paged_attention_decode (tokens = 0; max_context = columns of the block table x block size,
-    weights when mass is asked for) or of paged_attention_prefill (tokens = rows of q); None if it needs none."""
+    """Scratch of paged_attention_decode (tokens = 0; max_context = columns of the block table x block size, or with a
+    window as little as window + sinks + 96; weights when mass is asked for) or of paged_attention_prefill (tokens =
+    rows of q); None if it needs none."""
     with torch.cuda.device(device):
         n = fp8_paged_attention_workspace_size(B, Hq, H, Dh, max_context, weights, tokens)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
@@ -659,7 +660,8 @@ def paged_attention_decode(q, k_cache, v_cache, block_table, seq_lens, window=0,
     o = out if out is not None else q.new_empty((B, Hq, Dh))
     lse = q.new_empty((B, Hq), dtype=torch.float32)
     if workspace is None and B:
-        workspace = paged_attention_workspace(B, Hq, H, Dh, mb * k_cache.block_size, mass is not None, 0, q.device)
+        context = mb * k_cache.block_size if window <= 0 else min(mb * k_cache.block_size, window + sinks + 96)
+        workspace = paged_attention_workspace(B, Hq, H, Dh, context, mass is not None, 0, q.device)
     _dev_on(d, (*_cache_checks(caches), (block_table, torch.int32, "block_table"), (seq_lens, torch.int32, "seq_lens"),
                 (out, torch.bfloat16, "out"), (mass, torch.float32, "mass"), (workspace, torch.uint8, "workspace")))
     _decode_call(d, None, q, ld_q, B, Hq, caches, (H, Dh, k_cache.block_size, k_cache.num_blocks, k_cache.fmt),

@@ -595,8 +595,9 @@ FP8Q_API fp8_status fp8_paged_attention_prefill(
 
 /*
  * Workspace of the two attention calls on the current device: pass tokens = 0
- * for fp8_paged_attention_decode (max_context = max_blocks * block_size and
- * weights != 0 when mass is asked for), tokens = T for
+ * for fp8_paged_attention_decode (max_context = max_blocks * block_size, or
+ * window + sinks + 96 where a window is set and that is less; weights != 0 when
+ * mass is asked for), tokens = T for
  * fp8_paged_attention_prefill (max_context and weights are then ignored).
  * Apart from a few bytes per (sequence, query head) and the weights' scratch
  * the size does not grow with B.

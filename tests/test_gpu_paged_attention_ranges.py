@@ -223,3 +223,30 @@ def test_a_finite_query_row_leaves_the_others_their_bits(Dh, big):
         rows = [(t, 0, n - new + t) for t in (0, 16, 17, 18, 31, 63, 64, 80, 81, 99)]
         s = float(torch.tensor(scale))
         bounds.check(out, lse, q, k, v, table, [n], rows, s, 150, 2)
+
+
+# ---------------------------------------------------------------------------------- workspace of a window ----
+
+@pytest.mark.parametrize("window,sinks", [(100, 7), (1, 0), (64, 32), (97, 31)])
+def test_weights_with_a_window_need_scratch_for_the_window_alone(window, sinks):
+    """A long table, a short window: the scratch does not grow with the table, nothing is written behind it, and the
+    results are those with more."""
+    lens, H, G, Dh, bs = [5000, 300, 129], 4, 2, 64, 16
+    k, v, table, ln = make_caches(lens, H, Dh, bs, 0, seed=291)
+    q = inputs.normal_bf16((3, H * G, Dh), 1.0, seed=292).to(DEV)
+    full = fp8q.paged_attention_workspace(3, H * G, H, Dh, table.shape[1] * bs, True)
+    n = fp8q.paged_attention_workspace(3, H * G, H, Dh, window + sinks + 96, True).numel()
+    parts = fp8q.paged_attention_workspace(3, H * G, H, Dh, 0, True).numel()
+    assert n - parts < (full.numel() - parts) / 10
+    memory = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+    got = []
+    for ws in (full, memory[:n], None):
+        mass = torch.zeros((3, H, 5000), device=DEV)
+        out, lse = fp8q.paged_attention_decode(q, k, v, table, ln, window, sinks, mass=mass, workspace=ws)
+        got.append((out, lse, mass))
+    assert torch.all(memory[n:] == 0xA5)
+    for other in got[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(got[0], other))
+    with pytest.raises(fp8q.Fp8Error):
+        fp8q.paged_attention_decode(q, k, v, table, ln, window, sinks, mass=torch.zeros((3, H, 5000), device=DEV),
+                                    workspace=memory[:n - 256])
