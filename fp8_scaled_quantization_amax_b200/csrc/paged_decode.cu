@@ -35,10 +35,10 @@
 // per CTA, so the workspace does not grow with the batch.
 //
 // Measured on a B200 with L2 flushed: 32 sequences of up to 8192 tokens, 32
-// heads of 128, 1.12 GB in 190 us (5.9 TB/s, 0.91 of a copy); one of 131072
-// tokens, 8 heads with 8 query heads each, 277 MB in 59 us (55 of them in this
-// kernel, 12 of those before the first and after the last tile).  Tiles by TMA
-// instead of cp.async: 306 -> 235 us and 118 -> 97 us when they came in.
+// heads of 128, 1.12 GB in 196 - 202 us (5.6 TB/s, 0.87 of a copy); one of 131072
+// tokens, 8 heads with 8 query heads each, 277 MB in 60 - 62 us, 12 of those before
+// the first and after the last tile.  Tiles by TMA instead of cp.async: 306 -> 235
+// us and 118 -> 97 us when they came in; pages of 100 take 236 - 247 us today.
 #include <algorithm>
 #include <atomic>
 
@@ -896,7 +896,8 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 // Groups of up to 8 query heads take one column block, larger ones two (16
 // heads per pass over K and V; a head size of 256 has registers for one).
 // 16 x 8192 tokens, 8 KV heads of 128, 9, 16 and 32 query heads each: 85, 93 and
-// 153 us; with one block and more passes 89, 97 and 167 (heads of 64: 69 and 75).
+// 153 us; with one block and more passes 89, 97 and 167 (heads of 64: 69 and 75),
+// when that was chosen; 1 - 2 % more today.
 // A CTA's warps share out the largest power of two of heads that divides their
 // number, so that no warp is idle; the warps left per head take turns at its
 // tiles.

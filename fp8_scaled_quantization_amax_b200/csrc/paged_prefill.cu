@@ -14,8 +14,9 @@
 // 2^-11 each: in P they would cost a multiply and a shared load per weight),
 // against a running power of two of the largest scale so far.  Where the scales
 // of a run are too far apart for that, V is the codes and the scales multiply P,
-// each row by a power of two of its own.  Q is brought to
-// [2^14, 2^15) by a power of two.  The softmax reference is set to 2^7 below a
+// each row by a power of two of its own (8192 tokens: 2260 instead of 700 us).
+// Q is brought to [2^14, 2^15) by a power of two of the row tile, or of each row
+// where rows are more than 2^15 apart (1110 us).  The softmax reference is set to 2^7 below a
 // maximum and only moves when a tile's weights sum to 2^15, so neither the
 // maximum of a tile is looked for nor O rescaled but seldom, and weights are
 // exact to 2^-11 down to 2^-21 of the largest in fp16.
@@ -33,20 +34,25 @@
 // leave (O, reference, sum) in the workspace and k_prefill_join adds the parts in
 // the order of the CTAs.
 //
-// Measured on a B200, 32 query heads over 8 KV heads of 128: 8192 tokens 660 -
-// 690 us (800 - 830 TFLOP/s), tensor pipe 40 % busy, MUFU 40 %, issue slots 47 %.
+// Measured on a B200, 32 query heads over 8 KV heads of 128: 8192 tokens 700 -
+// 720 us (765 - 785 TFLOP/s), tensor pipe 39 % busy, MUFU 39 %, issue slots 46 %.
 // What bounds it is the chain of a row tile: softmax of 128 columns 2100 - 2600
 // cycles (128 exponentials of 8 cycles each and what they wait for), P to TMEM
 // 300, P V and the next S 1500 with their waits; two row tiles in turn take 4400 -
-// 5000 cycles where the tensor core needs 1024.  A unit costs 13000 - 17000
-// cycles more, for Q and the results.  Codes by TMA instead of cp.async: 1.01 ->
-// 0.97 ms when that came in.
+// 5000 cycles, where the tensor core needs 2048 (16 MMAs of 64 cycles for each) and
+// the exponentials 2048 as well.  The softmax threads and the look-up warps spill
+// (1240 bytes stored, 590 loaded in the code; 2.4 of 322 million warp instructions
+// executed are loads of spilled registers).  How the code lies in the instruction
+// cache, which four roles share, moves the time by 3 % either way.  A unit costs
+// 13000 - 17000 cycles more, for Q and the results.  Codes by TMA instead of
+// cp.async (pages that 8 does not divide): 700 against 1000 us.
 //
 // What a row must not see is kept out of it whatever it holds: S is masked by
 // selection; V rows of slots that are no live position are written as zeros;
 // and since a weight of zero does not hide a NaN or infinity in V, such values
 // in tiles that only part of the rows see are written as zeros as well, and
-// added to the rows that do see them at the end.
+// added to the rows that do see them at the end.  A V scale or a query row of
+// others decides at most which of the two ways above is taken.
 #include <algorithm>
 #include <atomic>
 
@@ -153,9 +159,13 @@ __device__ __forceinline__ bool tile_full(const PagedView &pv, const Unit &u, in
 }
 
 // A unit costs its tiles and this many more, for Q and the results.  Laid end to
-// end in cost, a unit's first kUnitCost places hold no tile.  8192 tokens (units
-// of 2 to 64 tiles) at 3, 4, 5, 6, 8: 766, 659, 661, 670, 710 us; few tokens over
-// a long cache and chunks with a window differ by less than 4 % from 3 to 8.
+// end in cost, a unit's first kUnitCost places hold no tile.  At 3, 4, 5, 6, 8:
+//   8192 tokens, 8 x 4 heads of 128     743   697  704  711  726 us
+//   2 x 5000 tokens, the same           638   596  594  599  618
+//   2048 tokens, the same                96    98  100  100  105
+//   16000 tokens, 8 heads of 64         579   583  586  589  596
+//   8192 tokens, 4 x 4 heads of 256    1143  1024  930  889  901
+// and a few tokens over a long cache, or chunks with a window, within 4 %.
 constexpr int kUnitCost = 5;
 
 constexpr int kPlanThreads = 1024;

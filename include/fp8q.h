@@ -550,9 +550,14 @@ FP8Q_API fp8_status fp8_paged_kv_gather(const uint8_t *cache, const float *scale
  *               between calls, but calls that may run at the same time (two
  *               streams, two graphs replayed together) need one each.
  *   Deterministic: the split over the cache's length depends on the lengths
- *   and the device only, and its parts are joined in a fixed order.  P and the
- *   products with V are fp16 tensor-core products with fp32 sums; logits,
- *   maxima and sums are fp32.
+ *   and the device only, and its parts are joined in a fixed order.
+ *   Accuracy: the products of Q with K (codes exact, Q to 2^-24 of its row's
+ *   largest element or better) and of P with V are fp16 tensor-core products
+ *   with fp32 sums; logits, maxima and sums are fp32, and a weight below 2^-126
+ *   of the query's largest may count as zero.  P takes V's scale: that product
+ *   is rounded to fp16 (2^-11) against the largest one of the query, in full
+ *   down to 2^-19 of it and off by 2^-30 of it below.  Values up to 2^90 in
+ *   magnitude keep every sum finite.
  *   Shapes: Dh % 16 == 0, 16 <= Dh <= 256, H * Dh <= 8192, Hq % H == 0,
  *   B <= 65535, B * Hq * Dh (rounded up to 64, 128 or 256) < 2^36,
  *   num_blocks * block_size < 2^31, max_blocks * block_size <= 2^31 - 65536,
@@ -583,8 +588,16 @@ FP8Q_API fp8_status fp8_paged_attention_decode(
  *             not written.
  *   out_bf16  [T, Hq, Dh] bf16, dense.  lse [T, Hq] fp32 or NULL.
  *   The remaining arguments, shapes, errors, determinism and the workspace are
- *   those of fp8_paged_attention_decode.  T * Hq <= 2^31 - 65536.  Here V's scales are
- *   applied to V in fp16 (two roundings of 2^-11), not to P.
+ *   those of fp8_paged_attention_decode.  T * Hq <= 2^31 - 65536.
+ *   Accuracy: as there, but V takes its scales, in fp16 (two roundings of 2^-11;
+ *   in E5M2 off by 2^-16 of the position's scale, the smallest code, besides), as
+ *   long as those that a thread block meets in one run of positions lie within
+ *   2^11 (E4M3) or 2^8 (E5M2) of each other; a position's weight is then off by
+ *   2^-32 where fp16's subnormals end.  Where they do not, P takes them as above,
+ *   off by 2^-37 of the largest product, and the call is up to three times as
+ *   slow.  Q keeps a row's elements in full down to 2^-16 of its largest and
+ *   loses at most 2^-24 of that below.  What a row does not see, and the other
+ *   rows, have no other part in its result.
  */
 FP8Q_API fp8_status fp8_paged_attention_prefill(
     const void *q_bf16, int64_t ld_q, int64_t T, const int64_t *q_offsets, int64_t B, int64_t Hq,
