@@ -29,6 +29,10 @@ inline FastDiv make_fastdiv(uint32_t d) {
     return {(uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1), s, d};
 }
 
+// A K scale as it multiplies a logit: an infinite one is a NaN, as the elements of q . k that it makes infinite are of
+// both signs.
+__device__ __forceinline__ float k_factor(float d) { return fmaf(d, 0.0f, d); }
+
 // The cache as one launch sees it.  Slot ids fit 31 bits (checked on the
 // host); byte offsets are formed in 64 bits.
 struct PagedView {

@@ -475,8 +475,8 @@ k_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtens
             bool up = false;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                const float dk0 = lds_f(ax + 4 * (16 * y + g));
-                const float dk1 = lds_f(ax + 4 * (16 * y + g + 8));
+                const float dk0 = k_factor(lds_f(ax + 4 * (16 * y + g)));
+                const float dk1 = k_factor(lds_f(ax + 4 * (16 * y + g + 8)));
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
 #pragma unroll

@@ -721,7 +721,7 @@ k_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
                     uint32_t mx = 0, mn = 0xFFFFFFFFu;        // of the finite scales; of those that are not zero
 #pragma unroll
                     for (int i = 0; i < KT / 32; ++i) {
-                        reinterpret_cast<float *>(m + P::M_DK)[32 * i + lane] = dk[i] * fabsf(a.scale) * kLog2e;
+                        reinterpret_cast<float *>(m + P::M_DK)[32 * i + lane] = k_factor(dk[i]) * fabsf(a.scale) * kLog2e;
                         reinterpret_cast<float *>(m + P::M_DV)[32 * i + lane] = dv[i];
                         reinterpret_cast<int *>(m + P::M_SLOT)[32 * i + lane] = s[i];
                         const uint32_t live = __ballot_sync(0xFFFFFFFFu, s[i] >= 0);

@@ -50,6 +50,27 @@ def test_visible_nan_beside_a_page_that_is_none(Dh, fmt, what):
         assert torch.equal(~ok, want)
 
 
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("Dh,fmt,j", [(64, 0, 0), (128, 1, 150), (256, 0, 199), (64, 1, 199)])
+def test_a_k_scale_that_is_not_finite(Dh, fmt, j, bad):
+    """The elements of q . k are infinite with both signs, or NaN: every query that sees the token gets NaN, whichever
+    sign the sum of its codes has, and no other query does."""
+    n, bs = 200, 16
+    k, v, table, ln = make_caches([n], 1, Dh, bs, fmt, seed=205)
+    blk, at = slot(table, 0, j, bs)
+    k.scale_inv[blk, at, 0] = bad
+    q = inputs.normal_bf16((n, 4, Dh), 1.0, seed=206).to(DEV)
+    for window, sinks in ((0, 0), (40, 2)):
+        out, lse = prefill(q, [0, n], k, v, table, ln, window, sinks)
+        one, l1 = fp8q.paged_attention_decode(q[-1:], k, v, table, ln, window, sinks)
+        p = torch.arange(n, device=DEV)
+        sees = (p >= j) & ((window == 0) | (j > p - window) | (j < sinks))
+        for x, y in ((out, lse), (one, l1)):
+            want = sees[-x.shape[0]:, None].expand(-1, 4)
+            assert torch.equal(torch.isnan(y), want) and torch.equal(torch.isnan(x.float()).all(-1), want)
+            assert torch.equal(torch.isnan(x.float()).any(-1), want)
+
+
 # ------------------------------------------------------------------------- V scales that are far apart ----
 
 @pytest.mark.parametrize("fmt", [0, 1])
