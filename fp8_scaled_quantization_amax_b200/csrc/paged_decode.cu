@@ -35,7 +35,7 @@
 // per CTA, so the workspace does not grow with the batch.
 //
 // Measured on a B200 with L2 flushed: 32 sequences of up to 8192 tokens, 32
-// heads of 128, 1.12 GB in 196 - 202 us (5.6 TB/s, 0.87 of a copy); one of 131072
+// heads of 128, 1.12 GB in 202 - 205 us (5.5 TB/s, 0.85 of a copy); one of 131072
 // tokens, 8 heads with 8 query heads each, 277 MB in 60 - 62 us, 12 of those before
 // the first and after the last tile.  Tiles by TMA instead of cp.async: 306 -> 235
 // us and 118 -> 97 us when they came in; pages of 100 take 236 - 247 us today.
@@ -43,7 +43,6 @@
 #include <atomic>
 
 #include "paged_attn.cuh"
-#include "tc.cuh"
 
 using namespace fp8q;
 
@@ -96,13 +95,6 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool liv
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -118,26 +110,6 @@ __device__ __forceinline__ float lds_f(uint32_t a) {
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
     return v;
 }
-// Four codes -> two fp16 pairs (exact).
-template <int FMT>
-__device__ __forceinline__ void to_f16x4(uint32_t c, uint32_t &lo, uint32_t &hi) {
-    if (FMT == FP8_E4M3)
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(c));
-    else
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-            "cvt.rn.f16x2.e5m2x2 %0, l;\n\tcvt.rn.f16x2.e5m2x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(c));
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 0 at -inf and below 2^-126
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile(
@@ -150,8 +122,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
-// 2^e for -126 <= e <= 127; infinity at 128
-__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // Visible positions of the one query of sequence b: [0, sinks) and [begin, n).
 // Its tiles hold 32 aligned positions each: those of the sinks, then those of

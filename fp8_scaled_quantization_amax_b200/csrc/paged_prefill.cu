@@ -57,7 +57,6 @@
 #include <atomic>
 
 #include "paged_attn.cuh"
-#include "tc.cuh"
 
 using namespace fp8q;
 
@@ -455,26 +454,6 @@ __device__ __forceinline__ uint64_t pack_ff(float lo, float hi) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
     return v;
 }
-__device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; 0 at -inf and below 2^-126
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 .. 127
-template <int FMT>
-__device__ __forceinline__ void to_f16x4(uint32_t c, uint32_t &lo, uint32_t &hi) {   // four codes, exact
-    if (FMT == FP8_E4M3)
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(c));
-    else
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-            "cvt.rn.f16x2.e5m2x2 %0, l;\n\tcvt.rn.f16x2.e5m2x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(c));
-}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -500,13 +479,6 @@ __device__ __forceinline__ void st_shared_u32(uint32_t a, uint32_t v) {
 }
 __device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Low and high words of the shared-memory descriptors, 128-byte swizzle.  K-major
@@ -1352,7 +1324,8 @@ cudaError_t launch_main(const PagedView &pv, const PrefillArgs &a, const Prefill
         cudaFuncAttributes fa;
         e = cudaFuncGetAttributes(&fa, k_prefill<FMT, DH, TMA>);
         if (e != cudaSuccess) return e;
-        if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;   // setmaxnreg needs exactly these
+        // the split adds up to what these give a block: with fewer, a warpgroup's share would be waited for for good
+        if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
         e = cudaFuncSetAttribute(k_prefill<FMT, DH, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::SMEM);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
